@@ -20,19 +20,23 @@ __all__ = ["kda_prefill", "kda_decode_step", "kda_prefill_workspace_size", "kda_
            "kda_prefill_workspace_min", "kda_set_wait_limit_ns", "kda_status_string", "kda_version", "KDAError",
            "library_path", "load_library", "KDA_OK", "KDA_ERR_INVALID_ARG",
            "KDA_ERR_UNSUPPORTED", "KDA_ERR_MISALIGNED", "KDA_ERR_WORKSPACE", "KDA_ERR_CUDA",
-           "KDA_ERR_TIMEOUT", "KDA_FLAG_NO_L2NORM", "KDA_FLAG_EXACT", "KDA_FLAG_SCALAR_GATE"]
+           "KDA_ERR_TIMEOUT", "KDA_FLAG_NO_L2NORM", "KDA_FLAG_EXACT", "KDA_FLAG_SCALAR_GATE", "KDA_FLAG_SOFTPLUS",
+           "kda_ssm_prefill", "kda_ssm_step"]
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_MISALIGNED = 0, 1, 2, 3
 KDA_ERR_WORKSPACE, KDA_ERR_CUDA, KDA_ERR_TIMEOUT = 4, 5, 6
 KDA_DTYPE_F32, KDA_DTYPE_BF16 = 0, 1
 KDA_FLAG_NO_L2NORM, KDA_FLAG_EXACT, KDA_FLAG_SCALAR_GATE = 0x1, 0x2, 0x4
+KDA_FLAG_SOFTPLUS = 0x8
+KDA_SSM_TILE = 128
 
 EXPORTED_SYMBOLS = ("kda_status_string", "kda_version", "kda_prefill_workspace_size",
                     "kda_prefill_workspace_min", "kda_prefill_launches", "kda_prefill",
                     "kda_prefill_ex", "kda_decode_step", "kda_decode_step_ex", "kda_device_error",
                     "kda_prefill_noalloc", "kda_short_conv_swish", "kda_short_conv_launches",
                     "kda_decode_step_conv", "kda_backward_workspace_size", "kda_backward",
-                    "kda_set_wait_limit_ns", "kda_prefill_conv")
+                    "kda_set_wait_limit_ns", "kda_prefill_conv", "kda_ssm_tile_states_size", "kda_ssm_prefill",
+                    "kda_ssm_step")
 
 
 class OutputGate(ctypes.Structure):
@@ -44,6 +48,13 @@ class ShortConv(ctypes.Structure):
     """``kda_short_conv``: causal short convolution + Swish (width, weight, states)."""
     _fields_ = [("width", ctypes.c_int32), ("weight", ctypes.c_void_p), ("state_in", ctypes.c_void_p),
                 ("state_out", ctypes.c_void_p)]
+
+
+class Ssm(ctypes.Structure):
+    """``kda_ssm``: sizes and parameters of a selective scan."""
+    _fields_ = [("channels", ctypes.c_int32), ("states", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("A", ctypes.c_void_p), ("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+
 
 _lib = None
 
@@ -115,6 +126,13 @@ def load_library():
     lib.kda_backward.restype = ctypes.c_int
     lib.kda_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.kda_set_wait_limit_ns.restype = ctypes.c_uint64
+    sp = ctypes.POINTER(Ssm)
+    lib.kda_ssm_tile_states_size.argtypes = [i64, i32, i32]
+    lib.kda_ssm_tile_states_size.restype = sz
+    lib.kda_ssm_prefill.argtypes = [vp, vp, vp, vp, vp, sp, fp, ip, i32, i64, ctypes.c_int, u32, vp, fp, fp, vp]
+    lib.kda_ssm_prefill.restype = ctypes.c_int
+    lib.kda_ssm_step.argtypes = [vp, vp, vp, vp, vp, sp, fp, i32, ctypes.c_int, u32, vp, vp]
+    lib.kda_ssm_step.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -365,3 +383,123 @@ def kda_backward(q, k, v, log_alpha, beta, do, dS_T=None, S0=None, cu_seqlens=No
     if rc != KDA_OK:
         raise KDAError(rc, "kda_backward")
     return dq, dkk, dvv, dla, db, dS0
+
+
+# ------------------------------------------------- the layer around the recurrences ----
+# These calls check shapes, dtypes and devices here (the C ABI sees only pointers), may be made on
+# tensors of a device other than the current one, and take what they allocate from the pool of the
+# stream they run on.
+
+class _On:
+    """Makes the tensors' device current, and ``stream`` if one is given, for the duration of a call."""
+
+    def __init__(self, device, stream):
+        self._device, self._stream = device, stream
+
+    def __enter__(self):
+        self._was = torch.cuda.current_device()
+        if self._was != self._device.index:
+            torch.cuda.set_device(self._device)
+        if self._stream is not None:
+            self._before = torch.cuda.current_stream(self._device)
+            torch.cuda.set_stream(self._stream)
+        return ctypes.c_void_p(torch.cuda.current_stream(self._device).cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            torch.cuda.set_stream(self._before)
+        if self._was != self._device.index:
+            torch.cuda.set_device(self._was)
+        return False
+
+
+def _arg(name, t, dtype, shape, device):
+    """The address of a contiguous ``t`` of this dtype and shape on this device (None: NULL)."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError("%s must live on %s, got %s" % (name, device, t.device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr() or None
+
+
+def _cuda(t):
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    return t.device
+
+
+def _seqs(cu_seqlens, device):
+    """(number of sequences, address) of an int32 ``cu_seqlens`` [N + 1] (None: one sequence)."""
+    if cu_seqlens is None:
+        return 1, None
+    return cu_seqlens.numel() - 1, _arg("cu_seqlens", cu_seqlens, torch.int32, (max(cu_seqlens.numel(), 2),), device)
+
+
+def _ssm(x, dt, B, C, A, z, D, dt_bias):
+    """Checks a scan's inputs; (device, rows, kda_ssm, addresses of x, dt, B, C, z)."""
+    dev = _cuda(x)
+    if x.dim() < 2 or B.dim() != 3 or A.dim() != 2:
+        raise ValueError("x must be [T, channels], B and C [T, groups, states], A [channels, states]")
+    T, (ch, n), f32 = x.shape[0], A.shape, torch.float32
+    if math.prod(x.shape[1:]) != ch:
+        raise ValueError("x must have the %d channels of A, got %s" % (ch, tuple(x.shape)))
+    bc = (T, B.shape[1], n)
+    p = Ssm(ch, n, B.shape[1], _arg("A", A, f32, (ch, n), dev), _arg("D", D, f32, (ch,), dev),
+            _arg("dt_bias", dt_bias, f32, (ch,), dev))
+    io = x.dtype
+    return dev, T, p, (_arg("x", x, io, x.shape, dev), _arg("dt", dt, io, x.shape, dev), _arg("B", B, io, bc, dev),
+                       _arg("C", C, io, bc, dev), _arg("z", z, io, x.shape, dev))
+
+
+def kda_ssm_prefill(x, dt, B, C, A, S0=None, cu_seqlens=None, *, D=None, dt_bias=None, z=None, softplus=True,
+                    save_states=False, y=None, S_T=None, stream=None):
+    """Selective state space scan over packed prompts (``kda_ssm_prefill`` in ``include/kda.h``).
+
+    x, dt, z ``[T, channels]`` (trailing axes may be split, as ``[T, H, d]``) and B, C
+    ``[T, groups, states]`` in bf16 or fp32; A ``[channels, states]``, D, dt_bias ``[channels]`` and
+    S0 ``[N, channels, states]`` fp32; cu_seqlens ``[N + 1]`` int32 on the device or None. Returns
+    ``(y, S_T)``, and with ``save_states`` the tile states that ``kda_ssm_backward`` reads as a third.
+    """
+    lib = load_library()
+    dev, T, p, (px, pdt, pB, pC, pz) = _ssm(x, dt, B, C, A, z, D, dt_bias)
+    code = _dtype_code(x)
+    N, pcu = _seqs(cu_seqlens, dev)
+    f32, st = torch.float32, (N, p.channels, p.states)
+    with _On(dev, stream) as on:
+        if y is None:
+            y = torch.empty_like(x)
+        if S_T is None:
+            S_T = torch.empty(st, dtype=f32, device=dev)
+        tiles = None
+        if save_states:
+            tiles = torch.empty((-(-T // KDA_SSM_TILE), p.channels, p.states), dtype=f32, device=dev)
+        rc = lib.kda_ssm_prefill(px, pdt, pB, pC, pz, ctypes.byref(p), _arg("S0", S0, f32, st, dev), pcu, N, T, code,
+                                 KDA_FLAG_SOFTPLUS if softplus else 0, _arg("y", y, x.dtype, x.shape, dev),
+                                 _arg("S_T", S_T, f32, st, dev), _arg("tile states", tiles, f32, getattr(tiles, "shape", None), dev), on)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_ssm_prefill")
+    return (y, S_T, tiles) if save_states else (y, S_T)
+
+
+def kda_ssm_step(x, dt, B, C, A, S, *, D=None, dt_bias=None, z=None, softplus=True, y=None, stream=None):
+    """One token of each sequence through the selective scan (``kda_ssm_step`` in ``include/kda.h``):
+    x, dt, z ``[N, channels]``, B, C ``[N, groups, states]``, S ``[N, channels, states]`` fp32 updated in
+    place. Returns y like x."""
+    lib = load_library()
+    dev, N, p, (px, pdt, pB, pC, pz) = _ssm(x, dt, B, C, A, z, D, dt_bias)
+    code = _dtype_code(x)
+    pS = _arg("S", S, torch.float32, (N, p.channels, p.states), dev)
+    with _On(dev, stream) as on:
+        if y is None:
+            y = torch.empty_like(x)
+        rc = lib.kda_ssm_step(px, pdt, pB, pC, pz, ctypes.byref(p), pS, N, code, KDA_FLAG_SOFTPLUS if softplus else 0,
+                              _arg("y", y, x.dtype, x.shape, dev), on)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_ssm_step")
+    return y

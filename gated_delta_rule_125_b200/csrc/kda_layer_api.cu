@@ -1,0 +1,77 @@
+// kda_layer_api.cu -- extern "C" boundary of the layer around the recurrences (selective scan,
+// short convolution with a bias and its backward, residual norms): host-side validation and
+// dispatch. Nothing here allocates device memory or synchronises.
+#include <stdint.h>
+
+#include "kda_layer.cuh"
+
+namespace {
+
+bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+template <typename... P> bool aligned16(const P *...p) { return (aligned(p, 16) && ...); }
+template <typename... P> bool aligned4(const P *...p) { return (aligned(p, 4) && ...); }
+
+bool known_dtype(kda_dtype t) { return t == KDA_DTYPE_F32 || t == KDA_DTYPE_BF16; }
+
+// Sizes that every selective scan call shares; `rows` is the number of tokens.
+kda_status check_ssm(const kda_ssm *p, int32_t num_seqs, int64_t rows, kda_dtype dtype, uint32_t flags) {
+    if (!p || num_seqs < 1 || num_seqs > 65535 || rows < 0) return KDA_ERR_INVALID_ARG;
+    if (!known_dtype(dtype) || (flags & ~(uint32_t)KDA_FLAG_SOFTPLUS)) return KDA_ERR_INVALID_ARG;
+    if (p->channels < 1 || p->groups < 1 || p->states < 1) return KDA_ERR_INVALID_ARG;
+    if (p->channels % p->groups || p->channels / p->groups % 8) return KDA_ERR_UNSUPPORTED;
+    if (p->states != 8 && p->states != 16 && p->states != 32 && p->states != 64 && p->states != 128)
+        return KDA_ERR_UNSUPPORTED;
+    if (rows > INT32_MAX || p->channels > (1 << 24)) return KDA_ERR_UNSUPPORTED;
+    if (rows > 0 && !p->A) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(p->A) || !aligned4(p->D, p->dt_bias)) return KDA_ERR_MISALIGNED;
+    return KDA_OK;
+}
+
+kda::SsmArgs ssm_args(const void *x, const void *dt, const void *B, const void *C, const void *z, const kda_ssm *p,
+                      int32_t N, int64_t total, uint32_t flags) {
+    kda::SsmArgs a{};
+    a.x = x; a.dt = dt; a.B = B; a.C = C; a.z = z;
+    a.A = p->A; a.D = p->D; a.dt_bias = p->dt_bias;
+    a.N = N; a.total = total;
+    a.channels = p->channels; a.states = p->states; a.groups = p->groups;
+    a.softplus = (flags & KDA_FLAG_SOFTPLUS) != 0;
+    return a;
+}
+
+kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_ssm_tile_states_size(int64_t total_tokens, int32_t channels, int32_t states) {
+    if (total_tokens < 0 || channels < 1 || states < 1) return 0;
+    return (size_t)((total_tokens + kda::kSsmTile - 1) / kda::kSsmTile) * channels * states * sizeof(float);
+}
+
+kda_status kda_ssm_prefill(const void *x, const void *dt, const void *B, const void *C, const void *z, const kda_ssm *ssm,
+                           const float *S0, const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                           kda_dtype dtype, uint32_t flags, void *y, float *S_T, float *tile_states,
+                           kda_stream_t stream) {
+    if (kda_status rc = check_ssm(ssm, num_seqs, total_tokens, dtype, flags); rc != KDA_OK) return rc;
+    if (!cu_seqlens && num_seqs != 1) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!x || !dt || !B || !C || !y)) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(x, dt, B, C, z, S0, cu_seqlens, y, S_T, tile_states)) return KDA_ERR_MISALIGNED;
+    kda::SsmArgs a = ssm_args(x, dt, B, C, z, ssm, num_seqs, total_tokens, flags);
+    a.S0 = S0; a.cu = cu_seqlens; a.y = y; a.S_T = S_T; a.tiles = tile_states;
+    return done(kda::ssm_prefill(a, dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_ssm_step(const void *x, const void *dt, const void *B, const void *C, const void *z, const kda_ssm *ssm,
+                        float *S, int32_t N, kda_dtype dtype, uint32_t flags, void *y, kda_stream_t stream) {
+    if (N < 1) return KDA_ERR_INVALID_ARG;
+    if (kda_status rc = check_ssm(ssm, 1, N, dtype, flags); rc != KDA_OK) return rc;
+    if (!x || !dt || !B || !C || !S || !y) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(x, dt, B, C, z, S, y)) return KDA_ERR_MISALIGNED;
+    kda::SsmArgs a = ssm_args(x, dt, B, C, z, ssm, N, N, flags);
+    a.S_T = S; a.y = y;
+    return done(kda::ssm_step(a, dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -367,6 +367,65 @@ kda_status kda_backward(const void *q, const void *k, const void *v, const float
                         float *grad_v, float *grad_log_alpha, float *grad_beta, float *grad_S0, void *workspace,
                         size_t workspace_bytes, kda_stream_t stream);
 
+/*
+ * Selective state space scan: the third recurrence of hybrid linear models beside KDA and GDN,
+ * diagonal per channel d and state n, its step, input and read-out weights chosen by the token:
+ *
+ *     delta_t[d] = softplus(dt_t[d] + dt_bias[d])     (without softplus unless KDA_FLAG_SOFTPLUS)
+ *     h_t[d][n]  = exp(delta_t[d] A[d][n]) h_{t-1}[d][n] + delta_t[d] x_t[d] B_t[g][n]
+ *     y_t[d]     = (sum_n C_t[g][n] h_t[d][n] + D[d] x_t[d]) * silu(z_t[d]),
+ *
+ * where g is the channel's group: `groups` runs of channels / groups channels share B and C. x is
+ * usually the output of the short convolution (kda_short_conv_swish). Arithmetic is fp32 for both
+ * dtypes; outputs are rounded once. Exponentials of delta A have a relative error of about 2^-22.
+ *
+ *   channels   a multiple of 8 * groups
+ *   states     8, 16, 32, 64 or 128 (KDA_ERR_UNSUPPORTED otherwise)
+ *   A          [channels][states] fp32, 16-byte aligned (decay rates: finite, normally < 0)
+ *   D          [channels] fp32 or NULL (0);  dt_bias [channels] fp32 or NULL (0); 4-byte aligned
+ */
+typedef struct kda_ssm {
+    int32_t channels;
+    int32_t states;
+    int32_t groups;
+    const float *A;
+    const float *D;
+    const float *dt_bias;
+} kda_ssm;
+
+/* flag of the kda_ssm_ entry points: delta = softplus(dt + dt_bias), else delta = dt + dt_bias */
+#define KDA_FLAG_SOFTPLUS 0x8
+
+/*
+ * The scan over packed prompts.
+ *
+ *   x, dt, y   [T][channels] dtype;   z likewise or NULL (no gate)
+ *   B, C       [T][groups][states] dtype
+ *   S0, S_T    [N][channels][states] fp32 initial / final states: NULL = zeros / not written; S_T
+ *              may alias S0. A sequence without tokens has S_T = S0.
+ *   cu_seqlens as for kda_prefill. Rows from cu_seqlens[N] on are neither read nor written.
+ *   tile_states  NULL, or [ceil(T / KDA_SSM_TILE)][channels][states] fp32, 16-byte aligned
+ *              (kda_ssm_tile_states_size bytes): the state before each tile of KDA_SSM_TILE tokens
+ *              of the packed axis, which kda_ssm_backward reads. Entries of tiles that start with
+ *              the first token of a sequence are unspecified.
+ *
+ * One launch, no workspace. Outputs must not overlap inputs (except S_T == S0).
+ */
+#define KDA_SSM_TILE 128
+size_t kda_ssm_tile_states_size(int64_t total_tokens, int32_t channels, int32_t states);
+kda_status kda_ssm_prefill(const void *x, const void *dt, const void *B, const void *C, const void *z,
+                           const kda_ssm *ssm, const float *S0, const int32_t *cu_seqlens,
+                           int32_t num_seqs, int64_t total_tokens, kda_dtype dtype, uint32_t flags,
+                           void *y, float *S_T, float *tile_states, kda_stream_t stream);
+
+/*
+ * One token of each of N sequences: x, dt, z, y [N][channels], B, C [N][groups][states] in dtype,
+ * S [N][channels][states] fp32 updated in place. One launch.
+ */
+kda_status kda_ssm_step(const void *x, const void *dt, const void *B, const void *C, const void *z,
+                        const kda_ssm *ssm, float *S, int32_t N, kda_dtype dtype, uint32_t flags, void *y,
+                        kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
