@@ -36,6 +36,7 @@ EXPORTED_SYMBOLS = ("kda_status_string", "kda_version", "kda_prefill_workspace_s
                     "kda_prefill_noalloc", "kda_short_conv_swish", "kda_short_conv_launches",
                     "kda_decode_step_conv", "kda_backward_workspace_size", "kda_backward",
                     "kda_set_wait_limit_ns", "kda_prefill_conv", "kda_ssm_tile_states_size", "kda_ssm_prefill",
+                    "kda_ssm_prefill_workspace_size", "kda_ssm_prefill_launches",
                     "kda_ssm_step")
 
 
@@ -129,7 +130,9 @@ def load_library():
     sp = ctypes.POINTER(Ssm)
     lib.kda_ssm_tile_states_size.argtypes = [i64, i32, i32]
     lib.kda_ssm_tile_states_size.restype = sz
-    lib.kda_ssm_prefill.argtypes = [vp, vp, vp, vp, vp, sp, fp, ip, i32, i64, ctypes.c_int, u32, vp, fp, fp, vp]
+    lib.kda_ssm_prefill_workspace_size.argtypes = lib.kda_ssm_prefill_launches.argtypes = [i32, i64, i32, i32, i32]
+    lib.kda_ssm_prefill_workspace_size.restype, lib.kda_ssm_prefill_launches.restype = sz, i64
+    lib.kda_ssm_prefill.argtypes = [vp, vp, vp, vp, vp, sp, fp, ip, i32, i64, ctypes.c_int, u32, vp, fp, fp, vp, sz, vp]
     lib.kda_ssm_prefill.restype = ctypes.c_int
     lib.kda_ssm_step.argtypes = [vp, vp, vp, vp, vp, sp, fp, i32, ctypes.c_int, u32, vp, vp]
     lib.kda_ssm_step.restype = ctypes.c_int
@@ -428,6 +431,13 @@ def _arg(name, t, dtype, shape, device):
     return t.data_ptr() or None
 
 
+def _scratch(workspace, device):
+    """(address, bytes) of a workspace tensor (None: none)."""
+    if workspace is None:
+        return None, 0
+    return _arg("workspace", workspace, workspace.dtype, workspace.shape, device), workspace.numel() * workspace.element_size()
+
+
 def _cuda(t):
     if not t.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
@@ -458,13 +468,14 @@ def _ssm(x, dt, B, C, A, z, D, dt_bias):
 
 
 def kda_ssm_prefill(x, dt, B, C, A, S0=None, cu_seqlens=None, *, D=None, dt_bias=None, z=None, softplus=True,
-                    save_states=False, y=None, S_T=None, stream=None):
+                    save_states=False, y=None, S_T=None, workspace=None, stream=None):
     """Selective state space scan over packed prompts (``kda_ssm_prefill`` in ``include/kda.h``).
 
     x, dt, z ``[T, channels]`` (trailing axes may be split, as ``[T, H, d]``) and B, C
     ``[T, groups, states]`` in bf16 or fp32; A ``[channels, states]``, D, dt_bias ``[channels]`` and
     S0 ``[N, channels, states]`` fp32; cu_seqlens ``[N + 1]`` int32 on the device or None. Returns
     ``(y, S_T)``, and with ``save_states`` the tile states that ``kda_ssm_backward`` reads as a third.
+    Outputs and the workspace are allocated with torch when not given.
     """
     lib = load_library()
     dev, T, p, (px, pdt, pB, pC, pz) = _ssm(x, dt, B, C, A, z, D, dt_bias)
@@ -476,12 +487,17 @@ def kda_ssm_prefill(x, dt, B, C, A, S0=None, cu_seqlens=None, *, D=None, dt_bias
             y = torch.empty_like(x)
         if S_T is None:
             S_T = torch.empty(st, dtype=f32, device=dev)
+        if workspace is None:
+            nbytes = lib.kda_ssm_prefill_workspace_size(N, T, p.channels, p.states, p.groups)
+            if nbytes:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         tiles = None
         if save_states:
             tiles = torch.empty((-(-T // KDA_SSM_TILE), p.channels, p.states), dtype=f32, device=dev)
         rc = lib.kda_ssm_prefill(px, pdt, pB, pC, pz, ctypes.byref(p), _arg("S0", S0, f32, st, dev), pcu, N, T, code,
                                  KDA_FLAG_SOFTPLUS if softplus else 0, _arg("y", y, x.dtype, x.shape, dev),
-                                 _arg("S_T", S_T, f32, st, dev), _arg("tile states", tiles, f32, getattr(tiles, "shape", None), dev), on)
+                                 _arg("S_T", S_T, f32, st, dev), _arg("tile states", tiles, f32, getattr(tiles, "shape", None), dev),
+                                 *_scratch(workspace, dev), on)
     if rc != KDA_OK:
         raise KDAError(rc, "kda_ssm_prefill")
     return (y, S_T, tiles) if save_states else (y, S_T)

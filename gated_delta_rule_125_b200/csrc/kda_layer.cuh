@@ -69,35 +69,56 @@ template <> struct Pack8<float> {
     }
 };
 
+// Copies 16 bytes to shared memory in the background (zeros where `on` is false).
+__device__ __forceinline__ void copy16(void *to, const void *from, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() {  // until at most the N last groups are in flight
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Eight channels by copy16, to a place that only this thread reads.
+template <typename T> __device__ __forceinline__ void copy8(Pack8<T> *to, const T *from, bool on) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(Pack8<T>) / 16; ++i)
+        copy16(reinterpret_cast<char *>(to) + 16 * i, reinterpret_cast<const char *>(from) + (on ? 16 * i : 0), on);
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {  // relative error about 2^-22
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+// e^v as 2^(v log2 e): relative error about 2^-22 + |v| 2^-24.
+__device__ __forceinline__ float exp_f(float v) { return exp2_approx(v * kLog2e); }
+__device__ __forceinline__ float rcp_approx(float x) {  // relative error about 2^-23; 0 for an infinite x
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // 1 / (1 + e^-v): for very negative v, e^-v = inf and the quotient is 0.
-__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + expf(-v)); }
+__device__ __forceinline__ float sigmoid_f(float v) { return rcp_approx(1.f + exp_f(-v)); }
 __device__ __forceinline__ float silu_f(float v) { return v * sigmoid_f(v); }
 
-// log(1 + e^v) = max(v, 0) + log1p(e^-|v|), with log1p(u) = 2 atanh(s), s = u / (2 + u) <= 1/3, by the
-// series of atanh (the first term left out is s^17 / 17 < 5e-10 of s): small results keep their
-// relative accuracy, which a logarithm of 1 + u would lose (a step delta of 0.001 is log(1.001)).
+// log(1 + e^v) = max(v, 0) + log1p(e^-|v|), with log1p(u) = 2 atanh(s), s = u / (2 + u) <= 1/3: small
+// results keep their relative accuracy, which a logarithm of 1 + u would lose (a step delta of 0.001 is
+// log(1.001)). atanh(s) / s is taken as the polynomial of degree 4 in s^2 that interpolates it at the
+// five Chebyshev points of [0, 1/9] (error below 2e-8).
 __device__ __forceinline__ float softplus_f(float v) {
-    const float u = expf(-fabsf(v));
-    const float s = __fdividef(u, 2.f + u), w = s * s;
-    float p = fmaf(w, 1.f / 15.f, 1.f / 13.f);
-    p = fmaf(w, p, 1.f / 11.f);
-    p = fmaf(w, p, 1.f / 9.f);
-    p = fmaf(w, p, 1.f / 7.f);
-    p = fmaf(w, p, 1.f / 5.f);
-    p = fmaf(w, p, 1.f / 3.f);
+    const float u = exp_f(-fabsf(v));
+    const float s = u * rcp_approx(2.f + u), w = s * s;
+    float p = fmaf(w, 0.1407888979f, 0.1398257911f);
+    p = fmaf(w, p, 0.2001229823f);
+    p = fmaf(w, p, 0.3333316147f);
     p = fmaf(w, p, 1.f);
     return fmaf(2.f * s, p, fmaxf(v, 0.f));
 }
-
-template <bool V> struct Bool {
-    static constexpr bool value = V;
-};
 
 // Two fp32 lanes in one instruction (fma.rn.f32x2 and friends of sm_100): half the issue slots.
 struct F2 {
@@ -122,6 +143,13 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     return r;
 }
 
+
+__device__ __forceinline__ F2 exp2_pair(F2 x) {
+    float a, b;
+    unpack(x, a, b);
+    return f2(exp2_approx(a), exp2_approx(b));
+}
+
 // ------------------------------------------------------------- selective scan ----
 
 constexpr int kSsmTile = 128;  // tokens of a tile (KDA_SSM_TILE)
@@ -139,7 +167,9 @@ struct SsmArgs {
     float *S_T;    // may be nullptr
     float *tiles;  // [ceil(total / kSsmTile)][channels][states]: states before each tile, or nullptr
 };
-cudaError_t ssm_prefill(const SsmArgs &a, bool bf16, cudaStream_t st);
+size_t ssm_prefill_workspace(int64_t total, int N, int channels, int states, int groups);
+int ssm_prefill_launches(int64_t total, int N, int channels, int states, int groups);
+cudaError_t ssm_prefill(const SsmArgs &a, void *ws, bool bf16, cudaStream_t st);
 // One token of each of N sequences: x, dt, z, y [N][channels], B, C [N][groups][states]; a.S_T in place.
 cudaError_t ssm_step(const SsmArgs &a, bool bf16, cudaStream_t st);
 
@@ -154,31 +184,6 @@ struct SsmBackwardArgs {
 };
 size_t ssm_backward_workspace(int64_t total, int N, int channels, int states, int groups);
 cudaError_t ssm_backward(const SsmBackwardArgs &b, bool bf16, cudaStream_t st);
-
-// Sequences of the packed axis dealt to R ranges of whole sequences: range r holds those whose first
-// token lies in [r T / R, (r + 1) T / R) (the last range also the empty ones behind the last token).
-struct SsmRange {
-    int s0, s1;      // sequences [s0, s1)
-    int64_t t0, t1;  // their tokens
-};
-__device__ __forceinline__ int lower_bound_cu(const int32_t *cu, int N, int64_t t) {  // first s with cu[s] >= t
-    int lo = 0, hi = N;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] >= t) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
-__device__ __forceinline__ SsmRange ssm_range(const int32_t *cu, int N, int64_t total, int r, int R) {
-    SsmRange g;
-    if (!cu) return SsmRange{0, 1, 0, total};
-    g.s0 = r == 0 ? 0 : lower_bound_cu(cu, N, total * r / R);
-    g.s1 = r == R - 1 ? N : lower_bound_cu(cu, N, total * (r + 1) / R);
-    g.t0 = cu[g.s0];
-    g.t1 = cu[g.s1];
-    return g;
-}
 
 // ---------------------------------------------------------- short convolution ----
 

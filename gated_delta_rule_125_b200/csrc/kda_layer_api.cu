@@ -15,14 +15,17 @@ template <typename... P> bool aligned4(const P *...p) { return (aligned(p, 4) &&
 bool known_dtype(kda_dtype t) { return t == KDA_DTYPE_F32 || t == KDA_DTYPE_BF16; }
 
 // Sizes that every selective scan call shares; `rows` is the number of tokens.
+kda_status check_ssm_sizes(int32_t num_seqs, int64_t rows, int32_t channels, int32_t states, int32_t groups) {
+    if (num_seqs < 1 || num_seqs > 65535 || rows < 0) return KDA_ERR_INVALID_ARG;
+    if (channels < 1 || groups < 1 || states < 1) return KDA_ERR_INVALID_ARG;
+    if (channels % groups || channels / groups % 8) return KDA_ERR_UNSUPPORTED;
+    if (states != 8 && states != 16 && states != 32 && states != 64 && states != 128) return KDA_ERR_UNSUPPORTED;
+    if (rows > INT32_MAX || channels > 65536) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
 kda_status check_ssm(const kda_ssm *p, int32_t num_seqs, int64_t rows, kda_dtype dtype, uint32_t flags) {
-    if (!p || num_seqs < 1 || num_seqs > 65535 || rows < 0) return KDA_ERR_INVALID_ARG;
-    if (!known_dtype(dtype) || (flags & ~(uint32_t)KDA_FLAG_SOFTPLUS)) return KDA_ERR_INVALID_ARG;
-    if (p->channels < 1 || p->groups < 1 || p->states < 1) return KDA_ERR_INVALID_ARG;
-    if (p->channels % p->groups || p->channels / p->groups % 8) return KDA_ERR_UNSUPPORTED;
-    if (p->states != 8 && p->states != 16 && p->states != 32 && p->states != 64 && p->states != 128)
-        return KDA_ERR_UNSUPPORTED;
-    if (rows > INT32_MAX || p->channels > (1 << 24)) return KDA_ERR_UNSUPPORTED;
+    if (!p || !known_dtype(dtype) || (flags & ~(uint32_t)KDA_FLAG_SOFTPLUS)) return KDA_ERR_INVALID_ARG;
+    if (kda_status rc = check_ssm_sizes(num_seqs, rows, p->channels, p->states, p->groups); rc != KDA_OK) return rc;
     if (rows > 0 && !p->A) return KDA_ERR_INVALID_ARG;
     if (!aligned16(p->A) || !aligned4(p->D, p->dt_bias)) return KDA_ERR_MISALIGNED;
     return KDA_OK;
@@ -50,17 +53,31 @@ size_t kda_ssm_tile_states_size(int64_t total_tokens, int32_t channels, int32_t 
     return (size_t)((total_tokens + kda::kSsmTile - 1) / kda::kSsmTile) * channels * states * sizeof(float);
 }
 
+size_t kda_ssm_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t states,
+                                      int32_t groups) {
+    if (check_ssm_sizes(num_seqs, total_tokens, channels, states, groups) != KDA_OK) return 0;
+    return kda::ssm_prefill_workspace(total_tokens, num_seqs, channels, states, groups);
+}
+
+int64_t kda_ssm_prefill_launches(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t states,
+                                 int32_t groups) {
+    if (check_ssm_sizes(num_seqs, total_tokens, channels, states, groups) != KDA_OK) return -1;
+    return kda::ssm_prefill_launches(total_tokens, num_seqs, channels, states, groups);
+}
+
 kda_status kda_ssm_prefill(const void *x, const void *dt, const void *B, const void *C, const void *z, const kda_ssm *ssm,
                            const float *S0, const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
-                           kda_dtype dtype, uint32_t flags, void *y, float *S_T, float *tile_states,
-                           kda_stream_t stream) {
+                           kda_dtype dtype, uint32_t flags, void *y, float *S_T, float *tile_states, void *workspace,
+                           size_t workspace_bytes, kda_stream_t stream) {
     if (kda_status rc = check_ssm(ssm, num_seqs, total_tokens, dtype, flags); rc != KDA_OK) return rc;
     if (!cu_seqlens && num_seqs != 1) return KDA_ERR_INVALID_ARG;
     if (total_tokens > 0 && (!x || !dt || !B || !C || !y)) return KDA_ERR_INVALID_ARG;
-    if (!aligned16(x, dt, B, C, z, S0, cu_seqlens, y, S_T, tile_states)) return KDA_ERR_MISALIGNED;
+    const size_t need = kda::ssm_prefill_workspace(total_tokens, num_seqs, ssm->channels, ssm->states, ssm->groups);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+    if (!aligned16(x, dt, B, C, z, S0, cu_seqlens, y, S_T, tile_states, workspace)) return KDA_ERR_MISALIGNED;
     kda::SsmArgs a = ssm_args(x, dt, B, C, z, ssm, num_seqs, total_tokens, flags);
     a.S0 = S0; a.cu = cu_seqlens; a.y = y; a.S_T = S_T; a.tiles = tile_states;
-    return done(kda::ssm_prefill(a, dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
+    return done(kda::ssm_prefill(a, workspace, dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kda_status kda_ssm_step(const void *x, const void *dt, const void *B, const void *C, const void *z, const kda_ssm *ssm,

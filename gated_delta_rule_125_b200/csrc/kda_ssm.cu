@@ -1,358 +1,443 @@
-// kda_ssm.cu -- the selective state space scan: packed prompts (ssm_prefill_kernel) and one
-// token of each sequence (ssm_step_kernel).
+// kda_ssm.cu -- the selective state space scan: packed prompts (ssm_scan_kernel) and one token of each
+// sequence (ssm_step_kernel).
 //
 //     delta = softplus(dt + dt_bias),  a_t = e^(delta_t A),  h_t = a_t h_(t-1) + delta_t x_t B_t,
 //     y_t = (sum_n C_t h_t + D x_t) silu(z_t)                per channel d and state n.
 //
-// Prompts. The recurrence is diagonal: per (token, channel, state) one exponential, three
-// multiply-adds and two multiplies, nothing a matrix instruction could take (the decay differs
-// per channel AND state). With 16 states the exponentials bound it: 16 per clock and SM.
+// Prompts. The recurrence is diagonal: per (token, channel, state) one exponential, two products and
+// two multiply-adds, nothing a matrix instruction could take (the decay differs per channel AND
+// state). With 16 states the exponentials bound it (16 per clock and SM: 8 clocks of a quarter SM for
+// a warp's 32; a quarter more for softplus and gate), before memory does (x, dt, z, y move once).
 //
-// A CTA owns CB channels and walks the tokens of its sequences in tiles of 128, TL lanes of K
-// consecutive tokens per channel (K TL = 128). Per state n a thread forms its K decays and inputs
-// once, in registers; folds them from a zero state; the TL lanes of a channel combine their
-// (decay product, end state) pairs by a shuffle scan; and each thread replays its tokens from the
-// state before them. So the time axis is parallel inside a tile and every exponential is taken
-// once: a split of the time axis into independent pieces would take each twice. The decay product
-// of a lane is one exponential of the sum of its steps, not a product of K roundings.
+// LPC lanes share a channel, NS states each, kept in registers as packed pairs (products and
+// multiply-adds two at a time), and walk the tokens of one sequence. Nothing but the chain of
+// multiply-adds waits for the token before: a batch's exponentials and products come first. The work
+// per (token, channel) -- softplus before, skip and gate after -- is done for a tile of 8 LPC tokens at
+// once, one token and 8 channels (a 16-byte vector of bf16) per thread; delta and delta x, and the sums
+// C h, pass through shared memory. Rows, B and C of the next tile are copied ahead by cp.async, each
+// thread to its own place; B and C are then expanded to fp32, read by all channels at one address.
 //
-// Memory: x, dt, z and y move once, as 16-byte vectors of 8 channels; delta and delta x go through
-// shared memory as fp32 [channel][token] (four tokens per load; a pad of 4 words per lane keeps the
-// lanes on different banks). B and C of a tile are transposed into shared memory as fp32
-// [state][token], 16 states at a time. The next tile's rows are loaded before the current tile is
-// worked on.
+// Where the channels alone do not fill the GPU the time axis is cut: one pass folds each segment from
+// a zero state into its end state and the sum of its steps (the decay of a whole segment is
+// e^(A sum delta), one exponential), ssm_join_kernel chains those, and the full pass starts each
+// segment from its true state. That takes the exponentials twice.
 //
-// Sequence edges inside a tile: the first token of a sequence has its decay replaced by 0 after
-// its own initial state went through it, so a tile may hold the end of one sequence, some short
-// ones and the start of another. Only tiles that hold an edge run that variant of the loop.
+// Measured, 8192 tokens x 4096 channels x 16 states, bf16 with a gate: 418 us, 68 % of the rate of
+// exponentials that its two passes take. What it replaced: the time axis parallel inside a tile, lanes
+// combining (decay product, end state) pairs by a shuffle scan, every exponential once: 525 us (14
+// instructions per element and 41 % of the issue slots, too few warps to hide its chains).
 #include "kda_layer.cuh"
 
 namespace kda {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kNB = 16;  // states of B and C held in shared memory at a time
+constexpr int kScanThreads = 128;
 
-template <int K, int TL> struct Lay {
-    static constexpr int kPad = K + 4;          // words per lane segment: 16-byte loads of all lanes hit different banks
-    static constexpr int kRow = TL * kPad;      // words per row of 128 tokens
-    static __device__ __forceinline__ int at(int t) { return t + (t / K) * 4; }
+// What a batch of SU tokens needs that no state enters: decays, inputs, read-out weights of a lane's
+// states. w = (delta, delta, delta x, delta x) of a token, bc = (B, B, C, C) per pair of states.
+template <int SU, int NP, int LPC> struct Batch {
+    F2 e[SU][NP], in[SU][NP], c[SU][NP];
+    __device__ __forceinline__ void load(const F2 (&A)[NP], const float *w, int ldw, const float *bc, int ldbc) {
+        F2 dl[SU];
+#pragma unroll
+        for (int u = 0; u < SU; ++u) {
+            const float4 v = *reinterpret_cast<const float4 *>(w + u * ldw);
+            dl[u] = f2(v.x, v.y);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const float4 g = *reinterpret_cast<const float4 *>(bc + u * ldbc + 4 * LPC * p);
+                in[u][p] = mul2(f2(v.z, v.w), f2(g.x, g.y));
+                c[u][p] = f2(g.z, g.w);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < SU; ++u)
+#pragma unroll
+            for (int p = 0; p < NP; ++p) e[u][p] = exp2_pair(mul2(dl[u], A[p]));
+    }
+    // the batch's steps; out = the lane's part of sum C h
+    template <bool READ> __device__ __forceinline__ void step(F2 (&h)[NP], int u, float &out) const {
+        F2 acc;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            h[p] = fma2(e[u][p], h[p], in[u][p]);
+            if (READ) acc = p ? fma2(c[u][p], h[p], acc) : mul2(c[u][p], h[p]);
+        }
+        if (READ) {
+            float lo, hi;
+            unpack(acc, lo, hi);
+            out = lo + hi;
+        }
+    }
 };
 
-size_t prefill_smem(int CB, int row, int states) {
-    return ((size_t)2 * CB * row + 16 + 2 * kNB * row + (size_t)2 * CB * states + 2 * kSsmTile) * 4;
+// Segment `slot` of the packed sequences: sequence s owns the slots from cu[s] / L + s on (its
+// ceil(length / L) segments fit before the next sequence's; the rest stay empty).
+struct Segment {
+    int s, seg, len;
+    int64_t t0;  // first token
+    bool last;
+};
+__device__ __forceinline__ Segment segment_of(const int32_t *cu, int N, int64_t total, int64_t slot, int L) {
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] / L + (int64_t)mid <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    const int64_t b = cu ? cu[lo] : 0, e = cu ? cu[lo + 1] : total;
+    Segment g;
+    g.s = lo;
+    g.seg = (int)(slot - (b / L + lo));
+    g.t0 = b + (int64_t)g.seg * L;
+    const int64_t left = e - g.t0;
+    g.len = (int)min((int64_t)L, left);
+    g.last = left <= L;
+    if (left <= 0 && !(g.seg == 0 && left == 0)) g.s = -1;  // an empty slot
+    return g;
 }
 
-template <typename T, int CB, int K, int TL>
-__global__ void __launch_bounds__(CB *TL)
-ssm_prefill_kernel(const SsmArgs a, const int bpg, const int R) {
-    using L = Lay<K, TL>;
-    constexpr int kRow = L::kRow;
-    constexpr int NT = CB * TL;
-    constexpr int U = kSsmTile * (CB / 8) / NT;   // (token, 8 channels) pieces per thread
-    constexpr int UB = kSsmTile * (kNB / 8) / NT; // (token, 8 states) pieces per thread
-    static_assert(K * TL == kSsmTile && U * NT == kSsmTile * (CB / 8) && UB * NT == kSsmTile * (kNB / 8), "shape");
-    extern __shared__ float4 smem4[];
-    float *sDt = reinterpret_cast<float *>(smem4);   // [CB][kRow] (8 channels, then 16 words, so that two pieces
-    float *sDx = sDt + CB * kRow + 8;                //  of a row do not meet on a bank)
-    float *sB = sDx + CB * kRow + 8;                 // [kNB][kRow]
-    float *sC = sB + kNB * kRow;
-    const int n = a.states;
-    float *sA = sC + kNB * kRow;                     // [CB][n], times log2 e
-    float *sH = sA + CB * n;                         // [CB][n], states before the tile
-    int *sFirst = reinterpret_cast<int *>(sH + CB * n);  // [128] sequence whose first token this is, or -1
-    int *sLast = sFirst + kSsmTile;
-    __shared__ int sNext;
+enum { kFull, kSave, kFold };  // y and final states; tile states too; only the segments' ends
 
-    const int tid = threadIdx.x, j = tid % TL, c = tid / TL;
-    const int cpg = a.channels / a.groups;
-    const int grp = blockIdx.x / bpg, cb = (blockIdx.x % bpg) * CB;  // channel block inside the group
-    const int d0 = grp * cpg + cb;
-    const int nc = min(CB, cpg - cb);  // channels of this block (a multiple of 8)
-    const T *x = static_cast<const T *>(a.x) + d0, *dt = static_cast<const T *>(a.dt) + d0;
-    const T *z = a.z ? static_cast<const T *>(a.z) + d0 : nullptr;
-    T *y = static_cast<T *>(a.y) + d0;
-    const size_t ldx = a.channels, ldb = (size_t)a.groups * n;
-    const T *Bp = static_cast<const T *>(a.B) + (size_t)grp * n, *Cp = static_cast<const T *>(a.C) + (size_t)grp * n;
+// Shared memory of a CTA, and the sizes that follow from the lanes per channel.
+template <typename T, int NS, int LPC, int MODE> struct ScanMem {
+    static constexpr int N_ = NS * LPC, CB = kScanThreads / LPC;  // states; channels of a CTA
+    static constexpr int TT = 8 * LPC;                  // tokens of a tile: one (token, 8 channels) piece per thread
+    static constexpr int UT = LPC > 8 ? LPC : 8;        // tokens of a group
+    static constexpr int BT0 = 512 / N_ > UT ? 512 / N_ : UT, BT = BT0 < TT ? BT0 : TT;  // tokens of B and C staged at a time
+    static constexpr int PIECES = BT * N_ / 8, PK = (PIECES + kScanThreads - 1) / kScanThreads;
+    static constexpr int kX = CB * 4 + 4, kY = CB + 4;  // words per token (padded: threads of consecutive tokens write)
+    static_assert(TT % BT == 0 && BT % UT == 0, "groups");
+    float sX[TT * kX];        // (delta, delta, delta x, delta x)
+    float sY[TT * kY];        // sum C h
+    float sBC[2][BT][2 * N_]; // (B, B, C, C) of two states
+    Pack8<T> sRow[2][MODE == kFold ? 2 : 3][kScanThreads];     // x, dt, z of the next tile: each thread's own piece
+    Pack8<T> sRaw[MODE == kFold ? 1 : 2][PK][kScanThreads];    // B and C likewise
+};
 
-    const SsmRange rg = ssm_range(a.cu, a.N, a.total, blockIdx.y, R);
-    const size_t nstate = (size_t)a.channels * n;
-    // sequences without tokens keep their initial state
-    if (a.S_T) {
-        for (int s = rg.s0; s < rg.s1; ++s) {
-            if ((a.cu ? (int64_t)a.cu[s + 1] - a.cu[s] : a.total) > 0) continue;
-            for (int i = tid; i < nc * n; i += NT) {
-                const size_t at = s * nstate + (size_t)d0 * n + i;
-                a.S_T[at] = a.S0 ? a.S0[at] : 0.f;
-            }
-        }
+template <typename T, int NS, int LPC, int MODE>
+__global__ void __launch_bounds__(kScanThreads, 4)
+ssm_scan_kernel(const SsmArgs a, const int nblk, const int bpg, const int L, float *__restrict__ seg_state,
+                float *__restrict__ seg_step) {
+    using M = ScanMem<T, NS, LPC, MODE>;
+    constexpr int N_ = M::N_, NP = NS / 2, CB = M::CB, TT = M::TT, UT = M::UT, BT = M::BT, PIECES = M::PIECES, PK = M::PK;
+    constexpr int kX = M::kX, kY = M::kY, SU = NP < 8 ? 8 / NP : 1;  // tokens of a batch: 8 pairs of states
+    extern __shared__ __align__(16) char smem_raw[];
+    M &sm = *reinterpret_cast<M *>(smem_raw);
+    auto &sX = sm.sX;
+    auto &sY = sm.sY;
+    auto &sBC = sm.sBC;
+    auto &sRow = sm.sRow;
+    auto &sRaw = sm.sRaw;
+    const int tid = threadIdx.x, q = tid % LPC, ch = tid / LPC;
+    const int blk = blockIdx.x % nblk;
+    const int64_t slot = blockIdx.x / nblk;
+    const Segment g = segment_of(a.cu, a.N, a.total, slot, L);
+    if (g.s < 0 || (MODE == kFold && g.last)) return;
+    const int64_t b = g.t0;
+    const int len = g.len;
+
+    const int cpg = a.channels / a.groups, grp = blk / bpg, c0 = (blk % bpg) * CB;
+    const int nc = min(CB, cpg - c0);  // channels of this block (a multiple of 8)
+    const bool on = ch < nc;
+    const int d0 = grp * cpg + c0;
+    const size_t ldx = a.channels, nstate = (size_t)a.channels * N_, own = (size_t)(d0 + (on ? ch : 0)) * N_ + q * NS;
+    F2 A[NP], h[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const float2 v = *reinterpret_cast<const float2 *>(a.A + own + 2 * p);
+        A[p] = f2(v.x * kLog2e, v.y * kLog2e);
+        h[p] = f2(0.f, 0.f);
+        const float *from = g.seg ? MODE == kFold ? nullptr : seg_state + (slot - 1) * nstate
+                                  : a.S0 ? a.S0 + g.s * nstate : nullptr;
+        if (from) h[p].v = *reinterpret_cast<const unsigned long long *>(from + own + 2 * p);
     }
-    if (rg.t1 <= rg.t0) return;
-    for (int i = tid; i < CB * n; i += NT) {
-        sA[i] = i < nc * n ? a.A[(size_t)d0 * n + i] * kLog2e : 0.f;
-        sH[i] = 0.f;
+    auto put = [&](float *to) {
+        if (!on) return;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) *reinterpret_cast<unsigned long long *>(to + own + 2 * p) = h[p].v;
+    };
+    if (len <= 0) {
+        if (a.S_T) put(a.S_T + g.s * nstate);
+        return;
     }
-    for (int i = tid; i < 2 * kSsmTile; i += NT) sFirst[i] = -1;
-    if (tid == 0) sNext = rg.s0;
 
-    Pack8<T> rx[U], rd[U], rb[UB], rc[UB];
-    auto load_rows = [&](int64_t t0) {
+    // this thread's piece of a tile: token pt, channels pc .. pc + 7
+    const int pt = tid % TT, pc = tid / TT * 8;
+    const bool pon = pc < nc;
+    const size_t at0 = (b + pt) * ldx + d0 + pc;
+    float bias[8], skip[8];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int p = tid + u * NT, c8 = (p / kSsmTile) * 8;
-            const int64_t t = t0 + p % kSsmTile;
-            if (t >= rg.t0 && t < rg.t1 && c8 < nc) {
-                rx[u].load(x + t * ldx + c8);
-                rd[u].load(dt + t * ldx + c8);
-            } else {
-                rx[u].zero();
-                rd[u].zero();
-            }
+    for (int i = 0; i < 8; ++i) {
+        bias[i] = pon && a.dt_bias ? a.dt_bias[d0 + pc + i] : 0.f;
+        skip[i] = pon && a.D ? a.D[d0 + pc + i] : 0.f;
+    }
+    const T *px = static_cast<const T *>(a.x) + at0, *pd = static_cast<const T *>(a.dt) + at0;
+    const T *pz = a.z ? static_cast<const T *>(a.z) + at0 : nullptr;
+    T *py = static_cast<T *>(a.y) + at0;
+    auto load_rows = [&](int t0, int st) {
+        const bool in = pon && t0 + pt < len;
+        copy8(&sRow[st][0][tid], in ? px + t0 * ldx : px, in);
+        copy8(&sRow[st][1][tid], in ? pd + t0 * ldx : pd, in);
+        if constexpr (MODE != kFold) {
+            if (pz) copy8(&sRow[st][2][tid], in ? pz + t0 * ldx : pz, in);
         }
+        copies_end_group();
     };
-    auto load_bc = [&](int64_t t0, int nb) {
+    const size_t ldb = (size_t)a.groups * N_;
+    const T *Bp = static_cast<const T *>(a.B) + b * ldb + (size_t)grp * N_, *Cp = static_cast<const T *>(a.C) + b * ldb + (size_t)grp * N_;
+    auto load_bc = [&](int t0) {
 #pragma unroll
-        for (int u = 0; u < UB; ++u) {
-            const int p = tid + u * NT, n8 = nb + (p / kSsmTile) * 8;
-            const int64_t t = t0 + p % kSsmTile;
-            if (t >= rg.t0 && t < rg.t1 && n8 < n) {
-                rb[u].load(Bp + t * ldb + n8);
-                rc[u].load(Cp + t * ldb + n8);
-            } else {
-                rb[u].zero();
-                rc[u].zero();
-            }
+        for (int u = 0; u < PK; ++u) {
+            const int p = tid + u * kScanThreads, t = t0 + p / (N_ / 8);
+            const bool in = p < PIECES && t < len;
+            const size_t at = in ? t * ldb + (p % (N_ / 8)) * 8 : 0;
+            copy8(&sRaw[0][u][tid], Bp + at, in);
+            if constexpr (MODE != kFold) copy8(&sRaw[1][u][tid], Cp + at, in);
         }
+        copies_end_group();
     };
-    auto store_bc = [&]() {
+    auto store_bc = [&](int buf) {
 #pragma unroll
-        for (int u = 0; u < UB; ++u) {
-            const int p = tid + u * NT, n8 = (p / kSsmTile) * 8, at = L::at(p % kSsmTile);
-            float v[8];
-            rb[u].get(v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sB[(n8 + i) * kRow + at] = v[i];
-            rc[u].get(v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sC[(n8 + i) * kRow + at] = v[i];
-        }
-    };
-    auto row = [&](int ch) { return ch * kRow + (ch / 8) * 8; };
-
-    const int64_t tile0 = rg.t0 / kSsmTile, tile1 = (rg.t1 + kSsmTile - 1) / kSsmTile;
-    load_rows(tile0 * kSsmTile);
-    load_bc(tile0 * kSsmTile, 0);
-    for (int64_t tile = tile0; tile < tile1; ++tile) {
-        const int64_t t0 = tile * kSsmTile;
-        const int64_t tb = max(t0, rg.t0), te = min(t0 + kSsmTile, rg.t1);
-        __syncthreads();  // the previous tile's y and marks have been read
-        const int s_from = sNext;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int p = tid + u * NT, c8 = (p / kSsmTile) * 8, at = L::at(p % kSsmTile);
-            const int64_t t = t0 + p % kSsmTile;
-            const bool in = t >= tb && t < te && c8 < nc;
+        for (int u = 0; u < PK; ++u) {
+            const int p = tid + u * kScanThreads;
+            if (p >= PIECES) continue;
             float v[8], w[8];
-            rd[u].get(v);
-            rx[u].get(w);
+            sRaw[0][u][tid].get(v);
+            if constexpr (MODE != kFold) sRaw[1][u][tid].get(w);
+            float4 *to = reinterpret_cast<float4 *>(&sBC[buf][p / (N_ / 8)][0]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pair = p % (N_ / 8) * 4 + i;  // pair pair % NP of lane pair / NP
+                to[pair % NP * LPC + pair / NP] = make_float4(v[2 * i], v[2 * i + 1], w[2 * i], w[2 * i + 1]);
+            }
+        }
+    };
+    load_rows(0, 0);
+    load_bc(0);
+    int buf = 0, st = 0;
+    float sum = 0.f;  // of the steps (kFold)
+    for (int t0 = 0; t0 < len; t0 += TT, st ^= 1) {
+        // before: steps and inputs of the tile (no step behind the last token)
+        copies_wait<1>();  // the rows (the first B and C of the tile may be in flight)
+        {
+            float xv[8], dl[8];
+            sRow[st][0][tid].get(xv);
+            sRow[st][1][tid].get(dl);
+            const bool in = t0 + pt < len;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dl[i] += bias[i];
+            if (a.softplus) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dl[i] = softplus_f(dl[i]);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                float dl = 0.f;
-                if (in) {
-                    dl = v[i] + (a.dt_bias ? a.dt_bias[d0 + c8 + i] : 0.f);
-                    if (a.softplus) dl = softplus_f(dl);
-                }
-                sDt[row(c8 + i) + at] = dl;
-                sDx[row(c8 + i) + at] = dl * w[i];
+                const float v = in ? dl[i] : 0.f, w = v * xv[i];
+                *reinterpret_cast<float4 *>(sX + pt * kX + (pc + i) * 4) = make_float4(v, v, w, w);
             }
         }
-        store_bc();
-        if (a.tiles && t0 >= rg.t0)
-            for (int i = tid; i < nc * n; i += NT) a.tiles[(size_t)tile * nstate + (size_t)d0 * n + i] = sH[i];
-        bool edge = false;
-        int next = s_from;
-        if (a.cu) {
-            for (int s = s_from + tid; s < rg.s1; s += NT) {
-                const int64_t b = a.cu[s], e = a.cu[s + 1];
-                if (b >= te) break;
-                if (e <= te) next = s + 1;
-                if (e <= b) continue;
-                if (b >= tb) sFirst[b - t0] = s, edge = true;
-                if (e <= te) sLast[e - 1 - t0] = s, edge = true;
-            }
-        } else if (tid == 0) {
-            if (tb == 0) sFirst[0] = 0, edge = true;
-            if (te == a.total) sLast[te - 1 - t0] = 0, edge = true;
-        }
-        edge = __syncthreads_or(edge);
-        if (next > s_from) atomicMax(&sNext, next);
-        if (tile + 1 < tile1) load_rows(t0 + kSsmTile);
-        if (n > kNB) load_bc(t0, kNB);
-        else if (tile + 1 < tile1) load_bc(t0 + kSsmTile, 0);
-
-        F2 dl[K / 2], dx[K / 2], yv[K / 2];
-        float sum = 0.f;
-        {
-            const float *pd = sDt + row(c) + j * L::kPad, *px = sDx + row(c) + j * L::kPad;
+        if (t0 + TT < len) load_rows(t0 + TT, st ^ 1);
+#pragma unroll 1
+        for (int v0 = 0; v0 < TT && t0 + v0 < len; v0 += BT, buf ^= 1) {
+            if (v0 == 0 && t0 + TT < len) copies_wait<1>();  // B and C (the next rows may be in flight)
+            else copies_wait<0>();
+            store_bc(buf);
+            __syncthreads();  // (the other buffer's readers have passed the barrier before)
+            if (t0 + v0 + BT < len) load_bc(t0 + v0 + BT);
+#pragma unroll 2
+            for (int v = 0; v < BT; v += UT) {  // (behind the last token: no steps, nothing stored)
+                const int tok = v0 + v;
+                const float *bc = &sBC[buf][v][q * 4];
+                float out[UT];
+                const int mark = MODE == kSave ? (int)(-(b + t0 + tok)) & (kSsmTile - 1) : kSsmTile;
 #pragma unroll
-            for (int k = 0; k < K; k += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(pd + k);
-                const float4 w = *reinterpret_cast<const float4 *>(px + k);
-                dl[k / 2] = f2(v.x, v.y);
-                dl[k / 2 + 1] = f2(v.z, v.w);
-                dx[k / 2] = f2(w.x, w.y);
-                dx[k / 2 + 1] = f2(w.z, w.w);
-                sum += (v.x + v.y) + (v.z + v.w);
-                yv[k / 2] = yv[k / 2 + 1] = f2(0.f, 0.f);
-            }
-        }
-        uint32_t first = 0, last = 0;
-        if (edge) {
+                for (int u0 = 0; u0 < UT; u0 += SU) {
+                    Batch<SU, NP, LPC> bt;
+                    bt.load(A, sX + (tok + u0) * kX + ch * 4, kX, bc + u0 * 2 * N_, 2 * N_);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                first |= (sFirst[j * K + k] >= 0 ? 1u : 0u) << k;
-                last |= (sLast[j * K + k] >= 0 ? 1u : 0u) << k;
-            }
-        }
-
-        auto states = [&](auto marked, int nb, int cnt) {
-            constexpr bool kMarked = decltype(marked)::value;
-            for (int i = 0; i < cnt; ++i) {
-                const float A2 = sA[c * n + nb + i], carry = sH[c * n + nb + i];
-                const float *pb = sB + i * kRow + j * L::kPad, *pc = sC + i * kRow + j * L::kPad;
-                float av[K], bv[K];
-                const F2 A22 = f2(A2, A2);
-#pragma unroll
-                for (int k = 0; k < K; k += 4) {
-                    const float4 b = *reinterpret_cast<const float4 *>(pb + k);
-                    float u0, u1;
-                    unpack(mul2(dl[k / 2], A22), u0, u1);
-                    av[k] = exp2_approx(u0);
-                    av[k + 1] = exp2_approx(u1);
-                    unpack(mul2(dl[k / 2 + 1], A22), u0, u1);
-                    av[k + 2] = exp2_approx(u0);
-                    av[k + 3] = exp2_approx(u1);
-                    unpack(mul2(dx[k / 2], f2(b.x, b.y)), bv[k], bv[k + 1]);
-                    unpack(mul2(dx[k / 2 + 1], f2(b.z, b.w)), bv[k + 2], bv[k + 3]);
-                }
-                float ap = exp2_approx(sum * A2);
-                if constexpr (kMarked) {
-                    if (first) {
-                        ap = 0.f;
-#pragma unroll
-                        for (int k = 0; k < K; ++k)
-                            if (first >> k & 1) {
-                                if (a.S0 && c < nc)
-                                    bv[k] = fmaf(av[k], a.S0[sFirst[j * K + k] * nstate + (size_t)(d0 + c) * n + nb + i], bv[k]);
-                                av[k] = 0.f;
-                            }
+                    for (int i = 0; i < SU; ++i) {
+                        const int u = u0 + i;
+                        if (MODE == kSave && u == mark && t0 + tok + u < len) put(a.tiles + (b + t0 + tok + u) / kSsmTile * nstate);
+                        bt.template step<MODE != kFold>(h, i, out[u]);
+                        if (MODE == kFold) sum += sX[(tok + u) * kX + ch * 4];
                     }
                 }
-                float e = bv[0];
+                if (MODE == kFold) continue;
+                // sums over the channel's lanes: lane q keeps the tokens u = q mod LPC
 #pragma unroll
-                for (int k = 1; k < K; ++k) e = fmaf(av[k], e, bv[k]);
-                if (j == 0) e = fmaf(ap, carry, e);
+                for (int m = LPC / 2; m > 0; m >>= 1) {
 #pragma unroll
-                for (int s = 1; s < TL; s <<= 1) {
-                    const float eo = __shfl_up_sync(0xffffffffu, e, s, TL), ao = __shfl_up_sync(0xffffffffu, ap, s, TL);
-                    if (j >= s) {
-                        e = fmaf(ap, eo, e);
-                        ap *= ao;
+                    for (int u = 0; u < UT; ++u) {
+                        if (u & m || u % LPC >= 2 * m) continue;
+                        const float give = q & m ? out[u] : out[u + m], keep = q & m ? out[u + m] : out[u];
+                        out[u] = keep + __shfl_xor_sync(0xffffffffu, give, m);
                     }
                 }
-                float h = __shfl_up_sync(0xffffffffu, e, 1, TL);
-                if (j == 0) h = carry;
-                if (j == TL - 1) sH[c * n + nb + i] = e;
 #pragma unroll
-                for (int k = 0; k < K; k += 4) {
-                    const float4 cc = *reinterpret_cast<const float4 *>(pc + k);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) bv[k + m] = h = fmaf(av[k + m], h, bv[k + m]);
-                    yv[k / 2] = fma2(f2(cc.x, cc.y), f2(bv[k], bv[k + 1]), yv[k / 2]);
-                    yv[k / 2 + 1] = fma2(f2(cc.z, cc.w), f2(bv[k + 2], bv[k + 3]), yv[k / 2 + 1]);
-                }
-                if constexpr (kMarked) {
-                    if (last && a.S_T && c < nc) {
-#pragma unroll
-                        for (int k = 0; k < K; ++k)
-                            if (last >> k & 1) a.S_T[sLast[j * K + k] * nstate + (size_t)(d0 + c) * n + nb + i] = bv[k];
-                    }
-                }
-            }
-        };
-        for (int nb = 0; nb < n; nb += kNB) {
-            if (nb) {
-                __syncthreads();
-                store_bc();
-                __syncthreads();
-                if (nb + kNB < n) load_bc(t0, nb + kNB);
-                else if (tile + 1 < tile1) load_bc(t0 + kSsmTile, 0);
-            }
-            const int cnt = min(kNB, n - nb);
-            if (edge) states(Bool<true>{}, nb, cnt);
-            else states(Bool<false>{}, nb, cnt);
-        }
-        {  // y over this thread's own delta segment
-            float *py = sDt + row(c) + j * L::kPad;
-#pragma unroll
-            for (int k = 0; k < K; k += 4) {
-                float4 v;
-                unpack(yv[k / 2], v.x, v.y);
-                unpack(yv[k / 2 + 1], v.z, v.w);
-                *reinterpret_cast<float4 *>(py + k) = v;
+                for (int k = 0; k < UT / LPC; ++k) sY[(tok + k * LPC + q) * kY + ch] = out[k * LPC];
             }
         }
         __syncthreads();
-        if (edge)
-            for (int i = tid; i < 2 * kSsmTile; i += NT) sFirst[i] = -1;
+        // after: skip, gate, store
+        if (MODE != kFold && pon && t0 + pt < len) {
+            float o[8], xv[8], zv[8];
+            sRow[st][0][tid].get(xv);
+            if constexpr (MODE != kFold) sRow[st][2][tid].get(zv);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int p = tid + u * NT, c8 = (p / kSsmTile) * 8, at = L::at(p % kSsmTile);
-            const int64_t t = t0 + p % kSsmTile;
-            if (t < tb || t >= te || c8 >= nc) continue;
-            Pack8<T> q;
-            float xv[8], v[8];
-            q.load(x + t * ldx + c8);
-            q.get(xv);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = fmaf(a.D ? a.D[d0 + c8 + i] : 0.f, xv[i], sDt[row(c8 + i) + at]);
-            if (z) {
-                q.load_stream(z + t * ldx + c8);
-                q.get(xv);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= silu_f(xv[i]);
+            for (int i = 0; i < 8; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(sY + pt * kY + pc + i);
+                o[i] = v.x, o[i + 1] = v.y, o[i + 2] = v.z, o[i + 3] = v.w;
             }
-            q.set(v);
-            q.store_stream(y + t * ldx + c8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                o[i] = fmaf(skip[i], xv[i], o[i]);
+                if (pz) o[i] *= silu_f(zv[i]);
+            }
+            Pack8<T> w;
+            w.set(o);
+            w.store_stream(py + t0 * ldx);
         }
+    }
+    if (MODE == kFold) {
+        put(seg_state + slot * nstate);
+        if (on && q == 0) seg_step[slot * ldx + d0 + ch] = sum;
+    } else if (g.last && a.S_T) {
+        put(a.S_T + g.s * nstate);
     }
 }
 
-template <typename T, int CB, int K, int TL>
-cudaError_t launch_prefill(const SsmArgs &a, int R, cudaStream_t st) {
-    const int cpg = a.channels / a.groups, bpg = (cpg + CB - 1) / CB;
-    const size_t smem = prefill_smem(CB, Lay<K, TL>::kRow, a.states);
-    auto kern = ssm_prefill_kernel<T, CB, K, TL>;
-    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); e != cudaSuccess)
-        return e;
-    kern<<<dim3(bpg * a.groups, R), CB * TL, smem, st>>>(a, bpg, R);
+// True states at the segments' ends: seg_state[k] += e^(A sum delta_k) seg_state[k - 1] along a sequence.
+__global__ void __launch_bounds__(kScanThreads)
+ssm_join_kernel(const SsmArgs a, const int L, float *__restrict__ seg_state, const float *__restrict__ seg_step) {
+    const size_t nstate = (size_t)a.channels * a.states;
+    const size_t i = ((size_t)blockIdx.x * kScanThreads + threadIdx.x) * 4;
+    const int s = blockIdx.y;
+    if (i >= nstate) return;
+    const int64_t b = a.cu ? a.cu[s] : 0, e = a.cu ? a.cu[s + 1] : a.total;
+    const int64_t slot = b / L + s;
+    const int inner = (int)((e - b + L - 1) / L) - 1;  // segments that another one follows
+    if (inner < 2) return;
+    const int d = (int)(i / a.states);
+    float4 A = *reinterpret_cast<const float4 *>(a.A + i);
+    A.x *= kLog2e; A.y *= kLog2e; A.z *= kLog2e; A.w *= kLog2e;
+    float4 h = *reinterpret_cast<const float4 *>(seg_state + slot * nstate + i);
+    constexpr int P = 4;  // segments loaded ahead
+    for (int k0 = 1; k0 < inner; k0 += P) {
+        float4 v[P];
+        float w[P];
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+            if (k0 + k < inner) {
+                v[k] = *reinterpret_cast<const float4 *>(seg_state + (slot + k0 + k) * nstate + i);
+                w[k] = seg_step[(slot + k0 + k) * a.channels + d];
+            }
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+            if (k0 + k < inner) {
+                h.x = fmaf(exp2_approx(A.x * w[k]), h.x, v[k].x);
+                h.y = fmaf(exp2_approx(A.y * w[k]), h.y, v[k].y);
+                h.z = fmaf(exp2_approx(A.z * w[k]), h.z, v[k].z);
+                h.w = fmaf(exp2_approx(A.w * w[k]), h.w, v[k].w);
+                *reinterpret_cast<float4 *>(seg_state + (slot + k0 + k) * nstate + i) = h;
+            }
+    }
+}
+
+// How the lanes and the time axis are dealt out.
+constexpr int kMinSegment = 256, kWantCtas = 148 * 8;
+struct Cut {
+    int lanes;  // lanes of a channel
+    int L;      // tokens of a segment
+    int nblk, bpg;
+    int64_t slots;
+    bool split;
+};
+int blocks_of(int channels, int groups, int lanes) {
+    const int CB = kScanThreads / lanes;
+    return (channels / groups + CB - 1) / CB * groups;
+}
+// 16 states: two lanes to a channel (the fewest shuffles and instructions) where that gives every SM
+// CTAs, else eight. 8192 tokens of 4096 channels: 418 us with two, 632 us with eight; 256 tokens of 128
+// channels: 37 us with two, 23 us with eight (of which about 20 are the host's). 64 states: sixteen
+// lanes 207 us, eight 216 us, four 269 us (6151 tokens of 1024 channels in 16 sequences).
+int lanes_of(int64_t total, int N, int channels, int states, int groups) {
+    switch (states) {
+    case 8: return 4;
+    case 16: return blocks_of(channels, groups, 2) * max((int64_t)N, total / kMinSegment) >= 2 * 148 ? 2 : 8;
+    case 64: return 16;
+    default: return 8;
+    }
+}
+// The time axis is cut when the sequences' channels give fewer CTAs than half of eight per SM (four at a
+// time are resident): 8192 tokens of 4096 channels 418 us against 490 us uncut (four lanes, its best).
+Cut cut_of(int64_t total, int N, int channels, int states, int groups) {
+    Cut c;
+    c.lanes = lanes_of(total, N, channels, states, groups);
+    c.nblk = blocks_of(channels, groups, c.lanes);
+    c.bpg = c.nblk / groups;
+    int64_t L = total;
+    if ((int64_t)N * c.nblk * 2 <= kWantCtas) {
+        const int TT = 8 * c.lanes;  // whole tiles
+        const int64_t segs = kWantCtas / c.nblk;  // of all sequences
+        L = ((total + segs - 1) / segs + TT - 1) / TT * TT;
+        L = max(L, (int64_t)kMinSegment);
+    }
+    c.split = L < total;
+    c.L = (int)max(min(L, total), (int64_t)1);
+    c.slots = total / c.L + N;
+    return c;
+}
+
+template <typename T, int NS, int LPC, int MODE>
+cudaError_t launch_mode(const SsmArgs &a, const Cut &c, unsigned grid, float *state, float *step, cudaStream_t st) {
+    auto kern = ssm_scan_kernel<T, NS, LPC, MODE>;
+    constexpr int bytes = sizeof(ScanMem<T, NS, LPC, MODE>);
+    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); e != cudaSuccess) return e;
+    kern<<<grid, kScanThreads, bytes, st>>>(a, c.nblk, c.bpg, c.L, state, step);
     return cudaGetLastError();
 }
 
+template <typename T, int NS, int LPC>
+cudaError_t launch_scan(const SsmArgs &a, const Cut &c, void *ws, cudaStream_t st) {
+    float *state = static_cast<float *>(ws), *step = state + (size_t)c.slots * a.channels * a.states;
+    const unsigned grid = (unsigned)(c.slots * c.nblk);
+    if (c.split) {
+        if (cudaError_t e = launch_mode<T, NS, LPC, kFold>(a, c, grid, state, step, st); e != cudaSuccess) return e;
+        const unsigned gx = (unsigned)(((size_t)a.channels * a.states / 4 + kScanThreads - 1) / kScanThreads);
+        if (a.total > 2 * (int64_t)c.L) ssm_join_kernel<<<dim3(gx, a.N), kScanThreads, 0, st>>>(a, c.L, state, step);
+    }
+    return a.tiles ? launch_mode<T, NS, LPC, kSave>(a, c, grid, state, step, st)
+                   : launch_mode<T, NS, LPC, kFull>(a, c, grid, state, step, st);
+}
+
 template <typename T>
-cudaError_t prefill_t(const SsmArgs &a, cudaStream_t st) {
-    const int cpg = a.channels / a.groups;
-    const int64_t wide = (int64_t)a.groups * ((cpg + 15) / 16);
-    const int64_t most = (a.total + kSsmTile - 1) / kSsmTile;
-    const int R = (int)max((int64_t)1, min((int64_t)a.N, min(most, (148 * 8 + wide - 1) / wide)));
-    if (wide * R >= 148) return launch_prefill<T, 16, 8, 16>(a, R, st);
-    return launch_prefill<T, 8, 8, 16>(a, R, st);
+cudaError_t prefill_t(const SsmArgs &a, void *ws, cudaStream_t st) {
+    const Cut c = cut_of(a.total, a.N, a.channels, a.states, a.groups);
+    switch (a.states) {
+    case 8: return launch_scan<T, 2, 4>(a, c, ws, st);
+    case 16: return c.lanes == 2 ? launch_scan<T, 8, 2>(a, c, ws, st) : launch_scan<T, 2, 8>(a, c, ws, st);
+    case 32: return launch_scan<T, 4, 8>(a, c, ws, st);
+    case 64: return launch_scan<T, 4, 16>(a, c, ws, st);
+    case 128: return launch_scan<T, 16, 8>(a, c, ws, st);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace
 
-cudaError_t ssm_prefill(const SsmArgs &a, bool bf16, cudaStream_t st) {
-    return bf16 ? prefill_t<__nv_bfloat16>(a, st) : prefill_t<float>(a, st);
+size_t ssm_prefill_workspace(int64_t total, int N, int channels, int states, int groups) {
+    const Cut c = cut_of(total, N, channels, states, groups);
+    return c.split ? ((size_t)c.slots * channels * (states + 1) * sizeof(float) + 15) / 16 * 16 : 0;
+}
+
+int ssm_prefill_launches(int64_t total, int N, int channels, int states, int groups) {
+    const Cut c = cut_of(total, N, channels, states, groups);
+    return c.split ? total > 2 * (int64_t)c.L ? 3 : 2 : 1;
+}
+
+cudaError_t ssm_prefill(const SsmArgs &a, void *ws, bool bf16, cudaStream_t st) {
+    return bf16 ? prefill_t<__nv_bfloat16>(a, ws, st) : prefill_t<float>(a, ws, st);
 }
 
 // ------------------------------------------------------------------- one token ----

@@ -409,14 +409,24 @@ typedef struct kda_ssm {
  *              of the packed axis, which kda_ssm_backward reads. Entries of tiles that start with
  *              the first token of a sequence are unspecified.
  *
- * One launch, no workspace. Outputs must not overlap inputs (except S_T == S0).
+ *   workspace  kda_ssm_prefill_workspace_size() bytes of device scratch, 16-byte aligned (NULL where
+ *              that is 0): 4 (states + 1) bytes per channel for each segment that long prompts are cut
+ *              into when their channels alone do not fill the GPU.
+ *
+ * Enqueued as kda_ssm_prefill_launches() kernels (1 to 3). Outputs must not overlap inputs (except
+ * S_T == S0). Results do not depend on what the workspace held.
  */
 #define KDA_SSM_TILE 128
 size_t kda_ssm_tile_states_size(int64_t total_tokens, int32_t channels, int32_t states);
+size_t kda_ssm_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t states,
+                                      int32_t groups);
+int64_t kda_ssm_prefill_launches(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t states,
+                                 int32_t groups);
 kda_status kda_ssm_prefill(const void *x, const void *dt, const void *B, const void *C, const void *z,
                            const kda_ssm *ssm, const float *S0, const int32_t *cu_seqlens,
                            int32_t num_seqs, int64_t total_tokens, kda_dtype dtype, uint32_t flags,
-                           void *y, float *S_T, float *tile_states, kda_stream_t stream);
+                           void *y, float *S_T, float *tile_states, void *workspace, size_t workspace_bytes,
+                           kda_stream_t stream);
 
 /*
  * One token of each of N sequences: x, dt, z, y [N][channels], B, C [N][groups][states] in dtype,

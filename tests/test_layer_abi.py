@@ -35,10 +35,10 @@ def ssm_struct(a):
 
 
 def ssm_prefill(lib, **over):
-    a = dict(SSM, S0=None, cu=None, T=128, y=A, S_T=A, tiles=None)
+    a = dict(SSM, S0=None, cu=None, T=4096, y=A, S_T=A, tiles=None, ws=A, wsb=1 << 40)
     a.update(over)
     return lib.kda_ssm_prefill(a["x"], a["dt"], a["B"], a["C"], a["z"], ssm_struct(a), a["S0"], a["cu"], a["N"], a["T"],
-                               a["dtype"], a["flags"], a["y"], a["S_T"], a["tiles"], None)
+                               a["dtype"], a["flags"], a["y"], a["S_T"], a["tiles"], a["ws"], a["wsb"], None)
 
 
 def ssm_step(lib, **over):
@@ -52,7 +52,8 @@ def ssm_step(lib, **over):
 @pytest.mark.parametrize("over,code", SSM_BAD + [
     (dict(N=0), INVALID), (dict(N=3), INVALID), (dict(N=65536, cu=A), INVALID), (dict(T=-1), INVALID),
     (dict(T=1 << 31), UNSUPPORTED), (dict(S0=A + 4), MISALIGNED), (dict(S_T=A + 8), MISALIGNED),
-    (dict(cu=A + 4, N=2), MISALIGNED), (dict(tiles=A + 4), MISALIGNED)])
+    (dict(cu=A + 4, N=2), MISALIGNED), (dict(tiles=A + 4), MISALIGNED),
+    (dict(ws=None), kda.KDA_ERR_WORKSPACE), (dict(wsb=64), kda.KDA_ERR_WORKSPACE), (dict(ws=A + 8), MISALIGNED)])
 def test_ssm_prefill_rejects(lib, over, code):
     assert ssm_prefill(lib, **over) == code
 

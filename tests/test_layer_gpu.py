@@ -239,3 +239,25 @@ def test_ssm_steps_continue_a_prompt():
         out.append(kda.kda_ssm_step(one["x"], one["dt"], one["B"], one["C"], k["A"], S, D=k["D"], dt_bias=k["dt_bias"],
                                     z=one["z"]))
     ssm_check(k, torch.cat(out), S, [60])
+
+
+@pytest.mark.parametrize("lengths,ch,n,groups,dtype", [
+    ([2100], 40, 16, 1, BF16),           # nine segments of 256 tokens, the last one short
+    ([700, 0, 1300, 256, 3], 24, 8, 1, F32), ([513], 48, 32, 2, F32), ([1030, 600], 16, 64, 1, BF16), ([800], 8, 128, 1, F32),
+    ([2048, 1, 512], 1024, 16, 2, BF16),  # two lanes to a channel
+])
+def test_ssm_prefill_segments(lengths, ch, n, groups, dtype):
+    """Long sequences cut into segments: outputs, final states and tile states."""
+    assert kda.load_library().kda_ssm_prefill_launches(len(lengths), sum(lengths), ch, n, groups) > 1
+    k = ssm_case(lengths, ch, n, groups, dtype, seed=n + 1)
+    nbytes = kda.load_library().kda_ssm_prefill_workspace_size(len(lengths), sum(lengths), ch, n, groups)
+    ws = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN where nothing is written
+    y, S_T, tiles = ssm_run(k, save_states=True, workspace=ws)
+    ssm_check(k, y, S_T, lengths)
+    h = ssm_host(k)
+    ref = L.ssm_states(**h)[::128]
+    mag = L.ssm_states(**{m: (np.abs(v) if m in ("x", "B", "S0") else v) for m, v in h.items()})[::128]
+    keep = [i for i, t in enumerate(range(0, sum(lengths), 128)) if t not in set(h["cu"][:-1])]
+    within(tiles[keep], ref[keep], mag[keep], max(lengths) + 64)
+    again = ssm_run(k, workspace=ws)
+    assert torch.equal(y, again[0]) and torch.equal(S_T, again[1])
