@@ -9,6 +9,7 @@ Build the library with ``python -m gated_delta_rule_125_b200.build``.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import math
 import os
@@ -21,7 +22,7 @@ __all__ = ["kda_prefill", "kda_decode_step", "kda_prefill_workspace_size", "kda_
            "library_path", "load_library", "KDA_OK", "KDA_ERR_INVALID_ARG",
            "KDA_ERR_UNSUPPORTED", "KDA_ERR_MISALIGNED", "KDA_ERR_WORKSPACE", "KDA_ERR_CUDA",
            "KDA_ERR_TIMEOUT", "KDA_FLAG_NO_L2NORM", "KDA_FLAG_EXACT", "KDA_FLAG_SCALAR_GATE", "KDA_FLAG_SOFTPLUS",
-           "kda_ssm_prefill", "kda_ssm_step"]
+           "kda_ssm_prefill", "kda_ssm_step", "kda_ssm_backward"]
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_MISALIGNED = 0, 1, 2, 3
 KDA_ERR_WORKSPACE, KDA_ERR_CUDA, KDA_ERR_TIMEOUT = 4, 5, 6
@@ -37,7 +38,7 @@ EXPORTED_SYMBOLS = ("kda_status_string", "kda_version", "kda_prefill_workspace_s
                     "kda_decode_step_conv", "kda_backward_workspace_size", "kda_backward",
                     "kda_set_wait_limit_ns", "kda_prefill_conv", "kda_ssm_tile_states_size", "kda_ssm_prefill",
                     "kda_ssm_prefill_workspace_size", "kda_ssm_prefill_launches",
-                    "kda_ssm_step")
+                    "kda_ssm_step", "kda_ssm_backward_workspace_size", "kda_ssm_backward")
 
 
 class OutputGate(ctypes.Structure):
@@ -55,6 +56,11 @@ class Ssm(ctypes.Structure):
     """``kda_ssm``: sizes and parameters of a selective scan."""
     _fields_ = [("channels", ctypes.c_int32), ("states", ctypes.c_int32), ("groups", ctypes.c_int32),
                 ("A", ctypes.c_void_p), ("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+
+
+class SsmGrads(ctypes.Structure):
+    """``kda_ssm_grads``: where the gradients of a selective scan go."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "ddt", "dB", "dC", "dz", "dA", "dD", "ddt_bias", "dS0")]
 
 
 _lib = None
@@ -136,6 +142,11 @@ def load_library():
     lib.kda_ssm_prefill.restype = ctypes.c_int
     lib.kda_ssm_step.argtypes = [vp, vp, vp, vp, vp, sp, fp, i32, ctypes.c_int, u32, vp, vp]
     lib.kda_ssm_step.restype = ctypes.c_int
+    lib.kda_ssm_backward_workspace_size.argtypes = [i32, i64, i32, i32, i32]
+    lib.kda_ssm_backward_workspace_size.restype = sz
+    lib.kda_ssm_backward.argtypes = [vp, vp, vp, vp, vp, sp, fp, ip, i32, i64, ctypes.c_int, u32, fp, vp, fp,
+                                     ctypes.POINTER(SsmGrads), vp, sz, vp]
+    lib.kda_ssm_backward.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -519,3 +530,34 @@ def kda_ssm_step(x, dt, B, C, A, S, *, D=None, dt_bias=None, z=None, softplus=Tr
     if rc != KDA_OK:
         raise KDAError(rc, "kda_ssm_step")
     return y
+
+
+SsmGradients = collections.namedtuple("SsmGradients", "dx ddt dB dC dz dA dD ddt_bias dS0")
+
+
+def kda_ssm_backward(x, dt, B, C, A, dy, tile_states, dS_T=None, S0=None, cu_seqlens=None, *, D=None, dt_bias=None,
+                     z=None, softplus=True, workspace=None, stream=None):
+    """Backward of ``kda_ssm_prefill`` (``kda_ssm_backward`` in ``include/kda.h``): the gradients of a loss
+    through y and S_T given ``dy = dL/dy`` (like x) and ``dS_T = dL/dS_T`` (fp32, None: zero), with the
+    ``tile_states`` that the forward call returned. Returns fp32 ``SsmGradients(dx, ddt, dB, dC, dz, dA, dD,
+    ddt_bias, dS0)``, each shaped like its input (None where that is None)."""
+    lib = load_library()
+    dev, T, p, (px, pdt, pB, pC, pz) = _ssm(x, dt, B, C, A, z, D, dt_bias)
+    code = _dtype_code(x)
+    N, pcu = _seqs(cu_seqlens, dev)
+    f32, st = torch.float32, (N, p.channels, p.states)
+    pt = _arg("tile_states", tile_states, f32, (-(-T // KDA_SSM_TILE), p.channels, p.states), dev)
+    pdy, pdS, pS0 = _arg("dy", dy, x.dtype, x.shape, dev), _arg("dS_T", dS_T, f32, st, dev), _arg("S0", S0, f32, st, dev)
+    with _On(dev, stream) as on:
+        g = SsmGradients(*(None if t is None else torch.empty(t.shape, dtype=f32, device=dev)
+                           for t in (x, dt, B, C, z, A, D, dt_bias, S0)))
+        if workspace is None:
+            nbytes = lib.kda_ssm_backward_workspace_size(N, T, p.channels, p.states, p.groups)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        rc = lib.kda_ssm_backward(px, pdt, pB, pC, pz, ctypes.byref(p), pS0, pcu, N, T, code,
+                                  KDA_FLAG_SOFTPLUS if softplus else 0, pt, pdy, pdS,
+                                  ctypes.byref(SsmGrads(*(None if t is None else t.data_ptr() or None for t in g))),
+                                  *_scratch(workspace, dev), on)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_ssm_backward")
+    return g

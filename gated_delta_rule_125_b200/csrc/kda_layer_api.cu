@@ -91,4 +91,37 @@ kda_status kda_ssm_step(const void *x, const void *dt, const void *B, const void
     return done(kda::ssm_step(a, dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t kda_ssm_backward_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t states,
+                                       int32_t groups) {
+    if (check_ssm_sizes(num_seqs, total_tokens, channels, states, groups) != KDA_OK) return 0;
+    return kda::ssm_backward_workspace(total_tokens, num_seqs, channels, states, groups);
+}
+
+kda_status kda_ssm_backward(const void *x, const void *dt, const void *B, const void *C, const void *z,
+                            const kda_ssm *ssm, const float *S0, const int32_t *cu_seqlens, int32_t num_seqs,
+                            int64_t total_tokens, kda_dtype dtype, uint32_t flags, const float *tile_states,
+                            const void *dy, const float *dS_T, const kda_ssm_grads *grads, void *workspace,
+                            size_t workspace_bytes, kda_stream_t stream) {
+    if (kda_status rc = check_ssm(ssm, num_seqs, total_tokens, dtype, flags); rc != KDA_OK) return rc;
+    if (!grads || !ssm->A || !grads->dA || (!cu_seqlens && num_seqs != 1)) return KDA_ERR_INVALID_ARG;
+    const kda_ssm_grads &o = *grads;
+    if (total_tokens > 0 && (!x || !dt || !B || !C || !dy || !tile_states || !o.dx || !o.ddt || !o.dB || !o.dC ||
+                             (z != nullptr) != (o.dz != nullptr)))
+        return KDA_ERR_INVALID_ARG;
+    const size_t need = kda::ssm_backward_workspace(total_tokens, num_seqs, ssm->channels, ssm->states, ssm->groups);
+    if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+    if (!aligned16(x, dt, B, C, z, S0, cu_seqlens, tile_states, dy, dS_T, workspace) ||
+        !aligned16(o.dx, o.ddt, o.dB, o.dC, o.dz, o.dA, o.dS0) || !aligned4(o.dD, o.ddt_bias))
+        return KDA_ERR_MISALIGNED;
+    kda::SsmBackwardArgs g{};
+    g.f = ssm_args(x, dt, B, C, z, ssm, num_seqs, total_tokens, flags);
+    g.f.S0 = S0; g.f.cu = cu_seqlens;
+    g.f.tiles = const_cast<float *>(tile_states);
+    g.dy = dy; g.dS_T = dS_T;
+    g.dx = o.dx; g.ddt = o.ddt; g.dB = o.dB; g.dC = o.dC; g.dz = o.dz;
+    g.dA = o.dA; g.dD = o.dD; g.ddt_bias = o.ddt_bias; g.dS0 = o.dS0;
+    g.ws = workspace;
+    return done(kda::ssm_backward(g, dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

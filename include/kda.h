@@ -436,6 +436,41 @@ kda_status kda_ssm_step(const void *x, const void *dt, const void *B, const void
                         const kda_ssm *ssm, float *S, int32_t N, kda_dtype dtype, uint32_t flags, void *y,
                         kda_stream_t stream);
 
+/*
+ * Gradients of a loss through y and S_T of kda_ssm_prefill, given dy = dL/dy [T][channels] (dtype) and
+ * dS_T = dL/dS_T [N][channels][states] fp32 (or NULL: zero). Inputs as for the forward call, with the
+ * tile_states that it wrote (T > 0: required). All gradients are fp32, shaped like their inputs:
+ *
+ *   dx, ddt, dz  [T][channels] (dz NULL iff z is);   dB, dC [T][groups][states]
+ *   dA [channels][states];   dD, ddt_bias [channels] or NULL (not written)
+ *   dS0 [N][channels][states] or NULL (not written)
+ *
+ * All but dD and ddt_bias 16-byte aligned. Rows from cu_seqlens[N] on are neither read nor written.
+ * Sums over channels, tokens and sequences are added in a fixed order (no atomics: the same bits every
+ * call). workspace: kda_ssm_backward_workspace_size() bytes, 16-byte aligned (partial sums: 8 states
+ * bytes per token for every 8 to 32 channels, and 4 (states + 2) per sequence and channel).
+ * Three launches (two without tokens).
+ */
+typedef struct kda_ssm_grads {
+    float *dx;
+    float *ddt;
+    float *dB;
+    float *dC;
+    float *dz;
+    float *dA;
+    float *dD;
+    float *ddt_bias;
+    float *dS0;
+} kda_ssm_grads;
+size_t kda_ssm_backward_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t channels,
+                                       int32_t states, int32_t groups);
+kda_status kda_ssm_backward(const void *x, const void *dt, const void *B, const void *C, const void *z,
+                            const kda_ssm *ssm, const float *S0, const int32_t *cu_seqlens,
+                            int32_t num_seqs, int64_t total_tokens, kda_dtype dtype, uint32_t flags,
+                            const float *tile_states, const void *dy, const float *dS_T,
+                            const kda_ssm_grads *grads, void *workspace, size_t workspace_bytes,
+                            kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -261,3 +261,155 @@ def test_ssm_prefill_segments(lengths, ch, n, groups, dtype):
     within(tiles[keep], ref[keep], mag[keep], max(lengths) + 64)
     again = ssm_run(k, workspace=ws)
     assert torch.equal(y, again[0]) and torch.equal(S_T, again[1])
+
+
+# ------------------------------------------------ selective scan, gradients ----
+
+def ssm_grad_run(k, dy, dS_T, **kw):
+    y, S_T, tiles = ssm_run(k, save_states=True)
+    g = kda.kda_ssm_backward(k["x"], k["dt"], k["B"], k["C"], k["A"], dy, tiles, dS_T, k["S0"], k["cu"], D=k["D"],
+                             dt_bias=k["dt_bias"], z=k["z"], softplus=k["soft"], **kw)
+    return g
+
+
+def ssm_grad_check(k, dy, dS_T, g, lengths, what=""):
+    """Each gradient against the formula's, by the magnitude of the terms it is a sum of: the backward over
+    absolute values (steps and decay rates keep their signs, their parts of a sum counted positive)."""
+    h = ssm_host(k)
+    ref = L.ssm_backward(dy=host(dy), dS_T=host(dS_T), **h)
+    mag = ssm_grad_magnitude(h, host(dy), host(dS_T))
+    chain = 2 * max(lengths + [0]) + 128
+    for n in ("dx", "ddt", "dB", "dC", "dz", "dA", "dD", "ddt_bias", "dS0"):
+        got = getattr(g, n)
+        if got is not None:
+            within(got, ref[n], mag[n], chain, what + " " + n)
+
+
+def ssm_grad_magnitude(h, dy, dS_T):
+    """The sums of L.ssm_backward with every term taken positive."""
+    a = {n: np.abs(v) if v is not None and n not in ("cu", "soft", "dt", "dt_bias", "A") else v for n, v in h.items()}
+    groups, per = h["B"].shape[1], h["x"].shape[1] // h["B"].shape[1]
+    raw = h["dt"] + (0 if h["dt_bias"] is None else h["dt_bias"])
+    delta = L.softplus(raw) if h["soft"] else np.abs(raw)
+    T, ch, n = h["x"].shape + (h["A"].shape[1],)
+    cu = [0, T] if h["cu"] is None else h["cu"]
+    Bd, Cd = np.repeat(a["B"], per, 1), np.repeat(a["C"], per, 1)
+    D = np.zeros(ch) if a["D"] is None else a["D"]
+    gate = np.ones((T, ch)) if h["z"] is None else np.abs(h["z"] * L.sigmoid(h["z"]))
+    m = {k: np.zeros(s) for k, s in dict(dx=(T, ch), ddt=(T, ch), dz=(T, ch), dA=(ch, n), dD=ch, ddt_bias=ch,
+                                         dS0=(len(cu) - 1, ch, n), dB=(T, ch, n), dC=(T, ch, n)).items()}
+    sig = L.sigmoid(raw) if h["soft"] else np.ones_like(raw)
+    for s in range(len(cu) - 1):
+        hs = [np.zeros((ch, n)) if a["S0"] is None else a["S0"][s]]
+        sign = 1.0 if h["soft"] else np.sign(raw)
+        for t in range(cu[s], cu[s + 1]):
+            hs.append(np.exp((delta[t] * (sign if np.isscalar(sign) else sign[t]))[:, None] * h["A"]) * hs[-1]
+                      + (delta[t] * a["x"][t])[:, None] * Bd[t])
+        G = np.zeros((ch, n)) if dS_T is None else np.abs(dS_T[s])
+        for t in range(cu[s + 1] - 1, cu[s] - 1, -1):
+            st, before = hs[t - cu[s] + 1], hs[t - cu[s]]
+            e = np.abs(dy[t]) * gate[t]
+            if h["z"] is not None:
+                m["dz"][t] = np.abs(dy[t]) * ((Cd[t] * st).sum(-1) + D * a["x"][t]) * (1 + a["z"][t])
+            G = G + Cd[t] * e[:, None]
+            dec = np.exp((delta[t] * (sign if np.isscalar(sign) else sign[t]))[:, None] * h["A"])
+            m["dC"][t], m["dB"][t] = st * e[:, None], G * (delta[t] * a["x"][t])[:, None]
+            gb, ga = (G * Bd[t]).sum(-1), G * before * dec
+            m["dx"][t] = delta[t] * gb + D * e
+            m["dD"] += e * a["x"][t]
+            m["dA"] += ga * delta[t][:, None]
+            m["ddt"][t] = ((ga * np.abs(h["A"])).sum(-1) + gb * a["x"][t]) * sig[t]
+            G = G * dec
+        m["dS0"][s] = G
+    m["ddt_bias"] = m["ddt"].sum(0)
+    m["dB"], m["dC"] = (m[k].reshape(T, groups, per, n).sum(2) for k in ("dB", "dC"))
+    return m
+
+
+def ssm_grad_case(lengths, ch, n, groups=1, dtype=F32, seed=0, dS=True, **kw):
+    k = ssm_case(lengths, ch, n, groups, dtype, seed=seed, **kw)
+    return k, randn(sum(lengths), ch, seed=seed + 20, dtype=dtype), randn(len(lengths), ch, n, seed=seed + 21) if dS else None
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lengths", [[1], [7], [8], [127], [128], [129], [300], [0, 5, 1, 0, 130, 128, 127, 0], [2] * 30 + [3, 0, 1]])
+def test_ssm_backward_lengths(lengths, dtype):
+    k, dy, dS = ssm_grad_case(lengths, 24, 16, dtype=dtype, seed=len(lengths))
+    ssm_grad_check(k, dy, dS, ssm_grad_run(k, dy, dS), lengths)
+
+
+@pytest.mark.parametrize("ch,n,groups", [(8, 8, 1), (96, 8, 3), (16, 32, 2), (40, 32, 1), (24, 64, 1), (48, 128, 2), (8 * 5 * 3, 16, 5)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_ssm_backward_shapes(ch, n, groups, dtype):
+    lengths = [70, 3, 66]
+    k, dy, dS = ssm_grad_case(lengths, ch, n, groups, dtype, seed=n)
+    ssm_grad_check(k, dy, dS, ssm_grad_run(k, dy, dS), lengths)
+
+
+@pytest.mark.parametrize("gate,start,skip,bias,soft,dS", [(0, 0, 0, 0, 1, 0), (1, 0, 1, 0, 1, 1), (0, 1, 0, 1, 1, 0), (1, 1, 1, 0, 0, 1)])
+def test_ssm_backward_options(gate, start, skip, bias, soft, dS):
+    lengths = [200, 57]
+    k, dy, d = ssm_grad_case(lengths, 32, 16, 2, BF16, seed=3, dS=bool(dS), gate=bool(gate), start=bool(start),
+                             skip=bool(skip), bias=bool(bias), soft=bool(soft))
+    g = ssm_grad_run(k, dy, d)
+    assert (g.dz is None, g.dS0 is None, g.dD is None, g.ddt_bias is None) == (not gate, not start, not skip, not bias)
+    ssm_grad_check(k, dy, d, g, lengths)
+
+
+def test_ssm_backward_long_sequences():
+    """Tile states of a forward that cut its sequences into segments."""
+    lengths = [1100, 0, 900]
+    k, dy, dS = ssm_grad_case(lengths, 16, 16, dtype=F32, seed=40)
+    assert kda.load_library().kda_ssm_prefill_launches(3, 2000, 16, 16, 1) > 1
+    ssm_grad_check(k, dy, dS, ssm_grad_run(k, dy, dS), lengths)
+
+
+def test_ssm_backward_same_bits_and_rows_behind():
+    lengths = [150, 90]
+    k, dy, dS = ssm_grad_case(lengths, 64, 16, dtype=BF16, seed=41)
+    a, b = ssm_grad_run(k, dy, dS), ssm_grad_run(k, dy, dS)
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
+    nan = float("nan")
+    pad = {m: torch.cat([k[m], torch.full_like(k[m][:70], nan)]) for m in ("x", "dt", "B", "C", "z")}
+    c = ssm_grad_run(dict(k, **pad), torch.cat([dy, torch.full_like(dy[:70], nan)]), dS)
+    for n, u, v in zip(a._fields, a, c):
+        assert torch.equal(u, v[:240] if n in ("dx", "ddt", "dz", "dB", "dC") else v), n
+
+
+def test_ssm_backward_differences():
+    """The gradient of a step along a direction against the difference of two forward runs."""
+    k, dy, dS = ssm_grad_case([90, 40], 16, 16, dtype=F32, seed=42)
+    g = ssm_grad_run(k, dy, dS)
+
+    def loss(c):
+        y, S = ssm_run(c)
+        return float((y.double() * dy).sum() + (S.double() * dS).sum())
+
+    for n, name in (("x", "dx"), ("dt", "ddt"), ("B", "dB"), ("C", "dC"), ("z", "dz"), ("A", "dA"), ("D", "dD"), ("dt_bias", "ddt_bias"), ("S0", "dS0")):
+        v = randn(*k[n].shape, seed=50)
+        h = 2.0 ** -8
+        up, down = loss(dict(k, **{n: k[n] + h * v})), loss(dict(k, **{n: k[n] - h * v}))
+        want = float((getattr(g, name).double() * v).sum())
+        # truncation h^2 (third derivatives of O(1) per unit direction, grown by the direction's length), rounding of
+        # the forward outputs 2^-20 of their size over 2 h
+        scale = float(getattr(g, name).double().norm() * v.double().norm()) + 1.0
+        assert abs((up - down) / (2 * h) - want) <= 3e-2 * scale, n
+
+
+def test_ssm_backward_graph():
+    """Captured together with its forward and replayed on other inputs."""
+    k, dy, dS = ssm_grad_case([200, 33], 64, 16, dtype=BF16, seed=43)
+    ssm_grad_run(k, dy, dS)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = ssm_grad_run(k, dy, dS)
+    new, dy2, dS2 = ssm_grad_case([200, 33], 64, 16, dtype=BF16, seed=44)
+    for m in ("x", "dt", "B", "C", "z", "S0"):
+        k[m].copy_(new[m])
+    dy.copy_(dy2)
+    gr.replay()
+    ref = ssm_grad_run(k, dy, dS)
+    for u, v in zip(out, ref):
+        assert torch.equal(u, v)
