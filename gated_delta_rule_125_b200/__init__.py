@@ -22,7 +22,8 @@ __all__ = ["kda_prefill", "kda_decode_step", "kda_prefill_workspace_size", "kda_
            "library_path", "load_library", "KDA_OK", "KDA_ERR_INVALID_ARG",
            "KDA_ERR_UNSUPPORTED", "KDA_ERR_MISALIGNED", "KDA_ERR_WORKSPACE", "KDA_ERR_CUDA",
            "KDA_ERR_TIMEOUT", "KDA_FLAG_NO_L2NORM", "KDA_FLAG_EXACT", "KDA_FLAG_SCALAR_GATE", "KDA_FLAG_SOFTPLUS",
-           "kda_ssm_prefill", "kda_ssm_step", "kda_ssm_backward"]
+           "kda_ssm_prefill", "kda_ssm_step", "kda_ssm_backward",
+           "kda_short_conv_step", "kda_short_conv_backward", "kda_residual_norm", "kda_residual_norm_backward"]
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_MISALIGNED = 0, 1, 2, 3
 KDA_ERR_WORKSPACE, KDA_ERR_CUDA, KDA_ERR_TIMEOUT = 4, 5, 6
@@ -38,7 +39,10 @@ EXPORTED_SYMBOLS = ("kda_status_string", "kda_version", "kda_prefill_workspace_s
                     "kda_decode_step_conv", "kda_backward_workspace_size", "kda_backward",
                     "kda_set_wait_limit_ns", "kda_prefill_conv", "kda_ssm_tile_states_size", "kda_ssm_prefill",
                     "kda_ssm_prefill_workspace_size", "kda_ssm_prefill_launches",
-                    "kda_ssm_step", "kda_ssm_backward_workspace_size", "kda_ssm_backward")
+                    "kda_ssm_step", "kda_ssm_backward_workspace_size", "kda_ssm_backward",
+                    "kda_short_conv_swish_ex", "kda_short_conv_step", "kda_short_conv_backward_workspace_size",
+                    "kda_short_conv_backward", "kda_residual_norm", "kda_residual_norm_backward_workspace_size",
+                    "kda_residual_norm_backward")
 
 
 class OutputGate(ctypes.Structure):
@@ -61,6 +65,14 @@ class Ssm(ctypes.Structure):
 class SsmGrads(ctypes.Structure):
     """``kda_ssm_grads``: where the gradients of a selective scan go."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "ddt", "dB", "dC", "dz", "dA", "dD", "ddt_bias", "dS0")]
+
+
+class ResidualNorm(ctypes.Structure):
+    """``kda_residual_norm_args``: inputs of the norms around a block."""
+    _fields_ = [("y", ctypes.c_void_p), ("r", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("w_post", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("w_pre", ctypes.c_void_p), ("res_scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("rows", ctypes.c_int64), ("D", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("res_dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -147,6 +159,22 @@ def load_library():
     lib.kda_ssm_backward.argtypes = [vp, vp, vp, vp, vp, sp, fp, ip, i32, i64, ctypes.c_int, u32, fp, vp, fp,
                                      ctypes.POINTER(SsmGrads), vp, sz, vp]
     lib.kda_ssm_backward.restype = ctypes.c_int
+    lib.kda_short_conv_swish_ex.argtypes = [vp, vp, sc, fp, ip, i32, i64, i32, ctypes.c_int, vp]
+    lib.kda_short_conv_swish_ex.restype = ctypes.c_int
+    lib.kda_short_conv_step.argtypes = [vp, vp, sc, fp, i32, i32, ctypes.c_int, vp]
+    lib.kda_short_conv_step.restype = ctypes.c_int
+    lib.kda_short_conv_backward_workspace_size.argtypes = [i64, i32, i32]
+    lib.kda_short_conv_backward_workspace_size.restype = sz
+    lib.kda_short_conv_backward.argtypes = [vp, sc, fp, ip, i32, i64, i32, ctypes.c_int, vp, ctypes.c_int, fp, fp, fp,
+                                            fp, vp, sz, vp]
+    lib.kda_short_conv_backward.restype = ctypes.c_int
+    rn = ctypes.POINTER(ResidualNorm)
+    lib.kda_residual_norm.argtypes = [rn, vp, vp, vp]
+    lib.kda_residual_norm.restype = ctypes.c_int
+    lib.kda_residual_norm_backward_workspace_size.argtypes = [i64, i32]
+    lib.kda_residual_norm_backward_workspace_size.restype = sz
+    lib.kda_residual_norm_backward.argtypes = [rn, vp, fp, fp, fp, fp, fp, fp, fp, vp, sz, vp]
+    lib.kda_residual_norm_backward.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -344,13 +372,16 @@ def kda_decode_step(q, k, v, log_alpha, beta, S, *, l2norm=True, o=None, out_gat
     return o
 
 
-def kda_short_conv_swish(x, weight, cu_seqlens=None, *, state_in=None, state_out=None, y=None,
+def kda_short_conv_swish(x, weight, cu_seqlens=None, *, state_in=None, state_out=None, bias=None, y=None,
                          stream=None):
     """Causal short convolution + Swish (``kda_short_conv_swish`` in ``include/kda.h``).
 
     x ``[T, C]`` (or ``[T, H, d]``, C = H * d) in bf16 or fp32, weight ``[C, W]`` fp32,
     states ``[N, W-1, C]`` in x's dtype (state_out may be state_in). Returns y like x.
+    With ``bias`` ``[C]`` fp32 (``kda_short_conv_swish_ex``) it is added before the Swish.
     """
+    if bias is not None:
+        return _conv_bias(x, weight, cu_seqlens, state_in, state_out, bias, y, stream)
     lib = load_library()
     T = x.shape[0]
     C = int(math.prod(x.shape[1:]))
@@ -560,4 +591,129 @@ def kda_ssm_backward(x, dt, B, C, A, dy, tile_states, dS_T=None, S0=None, cu_seq
                                   *_scratch(workspace, dev), on)
     if rc != KDA_OK:
         raise KDAError(rc, "kda_ssm_backward")
+    return g
+
+
+def _conv_args(x, weight, bias, num_seqs, state_in, state_out):
+    """Checks a convolution's inputs; (device, rows, C, dtype code, kda_short_conv, addresses of x and bias)."""
+    dev = _cuda(x)
+    if x.dim() < 2 or weight.dim() != 2:
+        raise ValueError("x must be [T, C], weight [C, W]")
+    T, C, W = x.shape[0], math.prod(x.shape[1:]), weight.shape[1]
+    st = (num_seqs, W - 1, C)
+    c = ShortConv(W, _arg("weight", weight, torch.float32, (C, W), dev), _arg("state_in", state_in, x.dtype, st, dev),
+                  _arg("state_out", state_out, x.dtype, st, dev))
+    return dev, T, C, _dtype_code(x), c, _arg("x", x, x.dtype, x.shape, dev), _arg("bias", bias, torch.float32, (C,), dev)
+
+
+def _conv_bias(x, weight, cu_seqlens, state_in, state_out, bias, y, stream):
+    lib = load_library()
+    N, pcu = _seqs(cu_seqlens, _cuda(x))
+    dev, T, C, code, c, px, pb = _conv_args(x, weight, bias, N, state_in, state_out)
+    with _On(dev, stream) as on:
+        if y is None:
+            y = torch.empty_like(x)
+        rc = lib.kda_short_conv_swish_ex(px, _arg("y", y, x.dtype, x.shape, dev), ctypes.byref(c), pb, pcu, N, T, C, code, on)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_short_conv_swish")
+    return y
+
+
+def kda_short_conv_step(x, weight, state, *, bias=None, y=None, stream=None):
+    """The short convolution + Swish of one token of each sequence (``kda_short_conv_step`` in
+    ``include/kda.h``): x ``[N, C]``, weight ``[C, W]`` and bias ``[C]`` fp32, state ``[N, W-1, C]`` in x's
+    dtype, shifted in place (None for W = 1). Returns y like x."""
+    lib = load_library()
+    dev, N, C, code, c, px, pb = _conv_args(x, weight, bias, x.shape[0], None, state)
+    with _On(dev, stream) as on:
+        if y is None:
+            y = torch.empty_like(x)
+        rc = lib.kda_short_conv_step(px, _arg("y", y, x.dtype, x.shape, dev), ctypes.byref(c), pb, N, C, code, on)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_short_conv_step")
+    return y
+
+
+def kda_short_conv_backward(x, weight, dy, cu_seqlens=None, *, bias=None, state_in=None, want_dstate=False,
+                            workspace=None, stream=None):
+    """Backward of ``kda_short_conv_swish`` (``kda_short_conv_backward`` in ``include/kda.h``) given
+    ``dy = dL/dy`` like x, in fp32 or x's dtype. Returns fp32 ``(dx like x, dweight [C, W], dbias [C] (None
+    without bias), dstate [N, W-1, C] (None unless want_dstate))``."""
+    lib = load_library()
+    N, pcu = _seqs(cu_seqlens, _cuda(x))
+    dev, T, C, code, c, px, pb = _conv_args(x, weight, bias, N, state_in, None)
+    f32 = dict(dtype=torch.float32, device=dev)
+    pdy = _arg("dy", dy, dy.dtype, x.shape, dev)
+    with _On(dev, stream) as on:
+        dx, dw = torch.empty(x.shape, **f32), torch.empty(weight.shape, **f32)
+        db = None if bias is None else torch.empty((C,), **f32)
+        ds = torch.empty((N, weight.shape[1] - 1, C), **f32) if want_dstate else None
+        if workspace is None:
+            nbytes = lib.kda_short_conv_backward_workspace_size(T, C, weight.shape[1])
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        rc = lib.kda_short_conv_backward(px, ctypes.byref(c), pb, pcu, N, T, C, code, pdy, _dtype_code(dy),
+                                         dx.data_ptr() or None, dw.data_ptr(), None if db is None else db.data_ptr(),
+                                         None if ds is None else ds.data_ptr() or None, *_scratch(workspace, dev), on)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_short_conv_backward")
+    return dx, dw, db, ds
+
+
+def _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps):
+    """Checks the norms' inputs; (device, kda_residual_norm_args, dtype of the residual stream)."""
+    dev = _cuda(y)
+    D, rows = y.shape[-1], math.prod(y.shape[:-1])
+    res = y.dtype if r is None else r.dtype
+    code = _dtype_code(y)
+    w = lambda n, t: _arg(n, t, torch.float32, (D,), dev)
+    return dev, ResidualNorm(_arg("y", y, y.dtype, y.shape, dev), _arg("r", r, res, y.shape, dev),
+                             _arg("gate", gate, y.dtype, y.shape, dev), w("w_post", w_post), w("scale", scale),
+                             w("w_pre", w_pre), float(res_scale), float(eps), rows, D, code,
+                             code if r is None else _dtype_code(r)), res
+
+
+def kda_residual_norm(y, r=None, w_pre=None, *, w_post=None, gate=None, scale=None, res_scale=1.0, eps=1e-6, x=None,
+                      r_out=None, stream=None):
+    """The norm after a block, its gate and residual scale, the residual stream and the norm before the
+    next block, in one pass (``kda_residual_norm`` in ``include/kda.h``):
+
+        r_out = res_scale * r + scale * sigmoid(gate) * RMSNorm(y) * w_post,   x = RMSNorm(r_out) * w_pre.
+
+    y, gate ``[..., D]`` in bf16 or fp32; r, r_out in y's dtype or fp32; w_post, scale, w_pre ``[D]`` fp32.
+    Each of r, w_pre, w_post, gate, scale may be None (no stream yet, no norm before, no norm after, no
+    gate, scale 1). Returns ``(x, r_out)`` (x None without w_pre); ``r_out`` may be ``r``."""
+    lib = load_library()
+    dev, a, res = _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps)
+    with _On(dev, stream) as on:
+        if x is None and w_pre is not None:
+            x = torch.empty_like(y)
+        if r_out is None:
+            r_out = torch.empty(y.shape, dtype=res, device=dev)
+        rc = lib.kda_residual_norm(ctypes.byref(a), _arg("x", x, y.dtype, y.shape, dev), _arg("r_out", r_out, res, y.shape, dev), on)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_residual_norm")
+    return x, r_out
+
+
+ResidualNormGradients = collections.namedtuple("ResidualNormGradients", "dy dr dgate dw_post dscale dw_pre")
+
+
+def kda_residual_norm_backward(y, r, w_pre, dx, dr_out=None, *, w_post=None, gate=None, scale=None, res_scale=1.0,
+                               eps=1e-6, workspace=None, stream=None):
+    """Backward of ``kda_residual_norm`` (``kda_residual_norm_backward`` in ``include/kda.h``) given
+    ``dx = dL/dx`` (like y; None without w_pre) and ``dr_out = dL/dr_out`` (fp32, None: zero). Returns fp32
+    ``ResidualNormGradients(dy, dr, dgate, dw_post, dscale, dw_pre)``, each None where its input is."""
+    lib = load_library()
+    dev, a, _ = _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps)
+    pdx, pdr = _arg("dx", dx, y.dtype, y.shape, dev), _arg("dr_out", dr_out, torch.float32, y.shape, dev)
+    with _On(dev, stream) as on:
+        g = ResidualNormGradients(*(None if t is None else torch.empty(t.shape, dtype=torch.float32, device=dev)
+                                    for t in (y, r, gate, w_post, scale, w_pre)))
+        if workspace is None:
+            nbytes = lib.kda_residual_norm_backward_workspace_size(a.rows, a.D)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        rc = lib.kda_residual_norm_backward(ctypes.byref(a), pdx, pdr, *(None if t is None else t.data_ptr() or None for t in g),
+                                            *_scratch(workspace, dev), on)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_residual_norm_backward")
     return g

@@ -1,0 +1,421 @@
+// kda_conv_layer.cu -- the short convolution + Swish with a bias, for one token of each sequence, and
+// its gradients:
+//
+//     v_t[c] = bias[c] + sum_j w[c][j] x_(t-W+1+j)[c],   y = v sigmoid(v),
+//     g = dy sigmoid(v) (1 + v (1 - sigmoid(v))),
+//     dx_t = sum_j w[j] g_(t+W-1-j) (tokens of the same sequence),  dw[j] = sum_t g_t x_(t-W+1+j),  dbias = sum g,
+//
+// rows before a sequence's first token being its initial state (which gets dx's share as dstate).
+//
+// All of it is bound by memory: x (and dy) read once, y (dx) written once. A thread owns 8 consecutive
+// channels (a 16-byte vector of bf16) of a run of consecutive tokens and keeps the window in registers.
+// It loads some rows ahead, so that enough bytes are in flight. The rows around its run that its
+// window needs are its neighbours' too and come from the L2 cache.
+#include <type_traits>
+
+#include "kda_layer.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 128;
+
+// The last s with cu[s] <= t: the sequence of token t (t < cu[N]; the empty ones before it are skipped).
+__device__ __forceinline__ int sequence_of(const int32_t *cu, int N, int64_t t) {
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Row `pos` of a sequence that starts at token b (pos < 0: from its initial state, or zero).
+template <int W, typename T>
+__device__ __forceinline__ void window_row(Pack8<T> &r, const T *x, const T *state, int64_t b, int64_t pos, int s, int C) {
+    if (pos >= 0) r.load(x + (size_t)(b + pos) * C);
+    else if (state) r.load(state + ((size_t)s * (W - 1) + (W - 1 + pos)) * C);
+    else r.zero();
+}
+
+template <int W> __device__ __forceinline__ void load_taps(const float *w, int c0, float (&tap)[W][8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) tap[j][i] = w[(size_t)(c0 + i) * W + j];
+}
+
+__device__ __forceinline__ void load_bias(const float *bias, int c0, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = bias ? bias[c0 + i] : 0.f;
+}
+
+// ---- prompts ----
+
+constexpr int kRun = 16;                                        // tokens of a thread's run
+constexpr int ahead(int W) { return W > 4 ? 1 : 4; }            // rows loaded ahead (wide windows take the registers)
+
+template <int W, typename T>
+__global__ void __launch_bounds__(kThreads)
+conv_bias_kernel(const ConvArgs a) {
+    constexpr int kAhead = ahead(W);
+    const int nv = a.C / 8;
+    const int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x, t0 = g / nv * kRun;
+    const int c0 = (int)(g % nv) * 8;
+    const int64_t rows = a.cu ? a.cu[a.N] : a.total;
+    if (t0 >= rows) return;
+    const T *x = static_cast<const T *>(a.x) + c0;
+    const T *st = a.state_in ? static_cast<const T *>(a.state_in) + c0 : nullptr;
+    T *y = static_cast<T *>(a.y) + c0;
+    float tap[W][8], bias[8];
+    load_taps<W>(a.w, c0, tap);
+    load_bias(a.bias, c0, bias);
+    int s = a.cu ? sequence_of(a.cu, a.N, t0) : 0;
+    int64_t b = a.cu ? a.cu[s] : 0, e = a.cu ? a.cu[s + 1] : a.total;
+    const int64_t t1 = min(t0 + kRun, rows);
+    Pack8<T> win[W];  // win[W - 1]: the current row
+    auto fill = [&](int64_t t) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) window_row<W, T>(win[j], x, st, b, t - b - (W - 1) + j, s, a.C);
+    };
+    fill(t0);
+    for (int64_t t = t0; t < t1; t += kAhead) {
+        Pack8<T> next[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) next[k].load(x + (size_t)min(t + k, t1 - 1) * a.C);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (t + k >= t1) break;
+            if (t + k == e) {
+                do {
+                    ++s;
+                    b = a.cu[s];
+                    e = a.cu[s + 1];
+                } while (e == b);
+                fill(t + k);
+            }
+            win[W - 1] = next[k];
+            float v[8], r[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = bias[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                win[j].get(r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = fmaf(tap[j][i], r[i], v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = silu_f(v[i]);
+            Pack8<T> o;
+            o.set(v);
+            o.store_stream(y + (size_t)(t + k) * a.C);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
+        }
+    }
+}
+
+// Each sequence's last W - 1 raw rows (a thread reads all of its rows before it writes: in place is safe).
+template <int W, typename T>
+__global__ void __launch_bounds__(kThreads)
+conv_last_kernel(const ConvArgs a) {
+    if constexpr (W > 1) {
+        const int nv = a.C / 8;
+        const int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+        if (g >= (int64_t)a.N * nv) return;
+        const int s = (int)(g / nv), c0 = (int)(g % nv) * 8;
+        const int64_t b = a.cu ? a.cu[s] : 0, e = a.cu ? a.cu[s + 1] : a.total;
+        const T *x = static_cast<const T *>(a.x) + c0;
+        const T *st = a.state_in ? static_cast<const T *>(a.state_in) + c0 : nullptr;
+        T *to = static_cast<T *>(a.state_out) + c0;
+        Pack8<T> r[W - 1];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) window_row<W, T>(r[j], x, st, b, e - b - (W - 1) + j, s, a.C);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) r[j].store(to + ((size_t)s * (W - 1) + j) * a.C);
+    }
+}
+
+// ---- one token of each sequence: window = state and the new row, the state shifted in place ----
+
+template <int W, typename T>
+__global__ void __launch_bounds__(kThreads)
+conv_step_kernel(const ConvArgs a) {
+    const int nv = a.C / 8, v0 = blockIdx.x * kThreads + threadIdx.x;
+    if (v0 >= nv) return;
+    const int c0 = v0 * 8;
+    const T *x = static_cast<const T *>(a.x) + c0;
+    T *st = static_cast<T *>(a.state_out) + c0, *y = static_cast<T *>(a.y) + c0;
+    float tap[W][8], bias[8];
+    load_taps<W>(a.w, c0, tap);
+    load_bias(a.bias, c0, bias);
+    for (int s = blockIdx.y; s < a.N; s += gridDim.y) {
+        Pack8<T> win[W];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) win[j].load(st + ((size_t)s * (W - 1) + j) * a.C);
+        win[W - 1].load(x + (size_t)s * a.C);
+        float v[8], r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = bias[i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            win[j].get(r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fmaf(tap[j][i], r[i], v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = silu_f(v[i]);
+        Pack8<T> o;
+        o.set(v);
+        o.store(y + (size_t)s * a.C);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) win[j + 1].store(st + ((size_t)s * (W - 1) + j) * a.C);
+    }
+}
+
+// ---- gradients ----
+//
+// A thread's run of kBackRun tokens takes the g of its tokens and of the W - 1 behind them (which the
+// next run forms too) and writes its dx. Its sums for dw and dbias go to the workspace, a row per run,
+// and conv_sum_kernel adds the runs in order. A sequence's dstate is written by the thread of its first
+// token, which holds the g of its first W - 1 tokens.
+
+constexpr int kBackRun = 64;
+
+template <int W, typename T, typename TG>
+__global__ void __launch_bounds__(kThreads)
+conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part) {
+    constexpr int kAhead = ahead(W);
+    const ConvArgs &a = p.f;
+    const int nv = a.C / 8;
+    const int64_t gid = (int64_t)blockIdx.x * kThreads + threadIdx.x, run = gid / nv, t0 = run * kBackRun;
+    if (t0 >= a.total) return;
+    const int c0 = (int)(gid % nv) * 8;
+    const int64_t rows = a.cu ? a.cu[a.N] : a.total;
+    const T *x = static_cast<const T *>(a.x) + c0;
+    const T *st = a.state_in ? static_cast<const T *>(a.state_in) + c0 : nullptr;
+    const TG *dy = static_cast<const TG *>(p.dy) + c0;
+    float tap[W][8], bias[8], dw[W][8], db[8];
+    load_taps<W>(a.w, c0, tap);
+    load_bias(a.bias, c0, bias);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        db[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+    }
+    if (t0 < rows) {
+        int s = a.cu ? sequence_of(a.cu, a.N, t0) : 0;
+        int64_t b = a.cu ? a.cu[s] : 0, e = a.cu ? a.cu[s + 1] : a.total;
+        const int64_t t1 = min(t0 + kBackRun, rows), tl = min(t1 + W - 1, rows);  // the run, and what its dx needs
+        Pack8<T> win[W];
+        float acc[W][8];  // acc[j]: dx of row t - (W - 1) + j, so far
+        auto start = [&](int64_t t) {  // the window of token t of the current sequence, nothing summed yet
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                window_row<W, T>(win[j], x, st, b, t - b - (W - 1) + j, s, a.C);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[j][i] = 0.f;
+            }
+        };
+        auto flush = [&](int64_t t, int j) {  // acc[j], of row t, is complete: dx, or a row of the initial state
+            Pack8<float> o;
+            o.set(acc[j]);
+            if (t >= b) {
+                if (t >= t0 && t < t1) o.store_stream(p.dx + (size_t)t * a.C + c0);
+            } else if (p.dstate && t0 <= b) {
+                o.store(p.dstate + ((size_t)s * (W - 1) + (t - b + W - 1)) * a.C + c0);
+            }
+        };
+        start(t0);
+        for (int64_t t = t0; t < tl; t += kAhead) {
+            Pack8<T> nx[kAhead];
+            Pack8<TG> ny[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const size_t at = (size_t)min(t + k, tl - 1) * a.C;
+                nx[k].load(x + at);
+                ny[k].load(dy + at);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int64_t tk = t + k;
+                if (tk >= tl) break;
+                if (tk == e) {  // the next sequence: what the last rows of this one have is all they get
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) flush(e - (W - 1) + j, j);
+                    if (tk >= t1) {
+                        t = tl;
+                        e = -1;
+                        break;
+                    }
+                    do {
+                        ++s;
+                        b = a.cu[s];
+                        e = a.cu[s + 1];
+                    } while (e == b);
+                    start(tk);
+                }
+                win[W - 1] = nx[k];
+                float v[8], r[8], g[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[i] = bias[i];
+                    acc[W - 1][i] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    win[j].get(r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = fmaf(tap[j][i], r[i], v[i]);
+                }
+                ny[k].get(g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float sg = sigmoid_f(v[i]);
+                    g[i] *= sg * fmaf(v[i], 1.f - sg, 1.f);
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[j][i] = fmaf(tap[j][i], g[i], acc[j][i]);
+                if (tk < t1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) db[i] += g[i];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        win[j].get(r);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dw[j][i] = fmaf(g[i], r[i], dw[j][i]);
+                    }
+                }
+                flush(tk - (W - 1), 0);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {
+                    win[j] = win[j + 1];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[j][i] = acc[j + 1][i];
+                }
+            }
+        }
+        if (e >= 0) {  // what is left: rows up to the last of the run (complete: their sequence, or the rows, end here)
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+                if (tl == e || tl - (W - 1) + j < t1) flush(tl - (W - 1) + j, j);
+        }
+    }
+    float *to = part + (size_t)run * (W + 1) * a.C + c0;
+#pragma unroll
+    for (int j = 0; j <= W; ++j) {
+        Pack8<float> o;
+        if (j < W) o.set(dw[j < W ? j : 0]);
+        else o.set(db);
+        o.store(to + (size_t)j * a.C);
+    }
+}
+
+// dw [C][W], dbias [C]: the runs' sums, added in order by kSumLanes threads per value and then over those.
+constexpr int kSumLanes = 8;
+__global__ void __launch_bounds__(256)
+conv_sum_kernel(const float *__restrict__ part, const int64_t runs, const int C, const int W, float *__restrict__ dw,
+                float *__restrict__ dbias) {
+    __shared__ float red[kSumLanes][32];
+    const int c = blockIdx.x * 32 + threadIdx.x % 32, lane = threadIdx.x / 32, j = blockIdx.y;
+    float v = 0.f;
+    if (c < C) {
+#pragma unroll 4
+        for (int64_t r = lane; r < runs; r += kSumLanes) v += part[((size_t)r * (W + 1) + j) * C + c];
+    }
+    red[lane][threadIdx.x % 32] = v;
+    __syncthreads();
+    if (lane || c >= C) return;
+#pragma unroll
+    for (int k = 1; k < kSumLanes; ++k) v += red[k][threadIdx.x];
+    if (j < W) dw[(size_t)c * W + j] = v;
+    else if (dbias) dbias[c] = v;
+}
+
+// A sequence without tokens passes nothing on to its initial state.
+template <int W>
+__global__ void __launch_bounds__(kThreads)
+conv_empty_kernel(const int32_t *cu, const int64_t total, float *dstate, const int C) {
+    const int s = blockIdx.y;
+    const int64_t len = cu ? (int64_t)cu[s + 1] - cu[s] : total;
+    if (len > 0) return;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i < (int64_t)(W - 1) * C / 4)
+        reinterpret_cast<float4 *>(dstate + (size_t)s * (W - 1) * C)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+unsigned blocks(int64_t n) { return (unsigned)((n + kThreads - 1) / kThreads); }
+
+template <int W, typename T> cudaError_t launch_bias(const ConvArgs &a, cudaStream_t st) {
+    const int nv = a.C / 8;
+    if (a.total > 0) conv_bias_kernel<W, T><<<blocks((a.total + kRun - 1) / kRun * nv), kThreads, 0, st>>>(a);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (W > 1 && a.state_out) conv_last_kernel<W, T><<<blocks((int64_t)a.N * nv), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int W, typename T> cudaError_t launch_step(const ConvArgs &a, cudaStream_t st) {
+    const unsigned gx = blocks(a.C / 8);
+    const unsigned gy = (unsigned)max(1, min(a.N, (int)((148 * 8 + gx - 1) / gx)));
+    conv_step_kernel<W, T><<<dim3(gx, gy), kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int W, typename T, typename TG> cudaError_t launch_back(const ConvBackwardArgs &p, cudaStream_t st) {
+    const ConvArgs &a = p.f;
+    const int64_t runs = (a.total + kBackRun - 1) / kBackRun;
+    float *part = static_cast<float *>(p.ws);
+    if (runs > 0) conv_backward_kernel<W, T, TG><<<blocks(runs * (a.C / 8)), kThreads, 0, st>>>(p, part);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    conv_sum_kernel<<<dim3((a.C + 31) / 32, W + 1), 256, 0, st>>>(part, runs, a.C, W, p.dw, p.dbias);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (W > 1 && p.dstate && (a.cu || a.total == 0))
+        conv_empty_kernel<W><<<dim3(blocks((int64_t)(W - 1) * a.C / 4), a.N), kThreads, 0, st>>>(a.cu, a.total, p.dstate, a.C);
+    return cudaGetLastError();
+}
+
+template <typename F> cudaError_t by_width(int W, F f) {
+    switch (W) {
+    case 1: return f(std::integral_constant<int, 1>{});
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 3: return f(std::integral_constant<int, 3>{});
+    case 4: return f(std::integral_constant<int, 4>{});
+    case 5: return f(std::integral_constant<int, 5>{});
+    case 6: return f(std::integral_constant<int, 6>{});
+    case 7: return f(std::integral_constant<int, 7>{});
+    case 8: return f(std::integral_constant<int, 8>{});
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t conv_bias(const ConvArgs &a, bool bf16, cudaStream_t st) {
+    return by_width(a.W, [&](auto w) {
+        return bf16 ? launch_bias<w.value, __nv_bfloat16>(a, st) : launch_bias<w.value, float>(a, st);
+    });
+}
+
+cudaError_t conv_step(const ConvArgs &a, bool bf16, cudaStream_t st) {
+    return by_width(a.W, [&](auto w) {
+        return bf16 ? launch_step<w.value, __nv_bfloat16>(a, st) : launch_step<w.value, float>(a, st);
+    });
+}
+
+size_t conv_backward_workspace(int64_t total, int C, int W) {
+    return (size_t)((total + kBackRun - 1) / kBackRun) * (W + 1) * C * sizeof(float);
+}
+
+cudaError_t conv_backward(const ConvBackwardArgs &p, bool bf16, cudaStream_t st) {
+    return by_width(p.f.W, [&](auto w) {
+        if (!bf16) return launch_back<w.value, float, float>(p, st);
+        return p.dy_bf16 ? launch_back<w.value, __nv_bfloat16, __nv_bfloat16>(p, st)
+                         : launch_back<w.value, __nv_bfloat16, float>(p, st);
+    });
+}
+
+}  // namespace kda

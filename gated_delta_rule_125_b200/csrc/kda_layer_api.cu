@@ -42,6 +42,51 @@ kda::SsmArgs ssm_args(const void *x, const void *dt, const void *B, const void *
     return a;
 }
 
+// What every short convolution call shares.
+kda_status check_conv(const kda_short_conv *conv, const float *bias, int32_t num_seqs, int64_t rows, int32_t channels,
+                      kda_dtype dtype) {
+    if (!conv || num_seqs < 1 || rows < 0 || channels < 8 || channels % 8 || !known_dtype(dtype)) return KDA_ERR_INVALID_ARG;
+    if (conv->width < 1 || conv->width > KDA_MAX_CONV_WIDTH) return KDA_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || rows > INT32_MAX || channels > (1 << 20)) return KDA_ERR_UNSUPPORTED;
+    if (rows > 0 && !conv->weight) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(conv->state_in, conv->state_out) || !aligned4(conv->weight, bias)) return KDA_ERR_MISALIGNED;
+    return KDA_OK;
+}
+
+kda::ConvArgs conv_args(const void *x, void *y, const kda_short_conv *conv, const float *bias, const int32_t *cu,
+                        int32_t N, int64_t total, int32_t C) {
+    kda::ConvArgs a{};
+    a.x = x; a.y = y; a.w = conv->weight; a.bias = bias;
+    a.state_in = conv->state_in; a.state_out = conv->state_out;
+    a.cu = cu; a.N = N; a.total = total; a.C = C; a.W = conv->width;
+    return a;
+}
+
+bool overlap(const void *p, const void *q, size_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + bytes && b < a + bytes;
+}
+size_t size_of(kda_dtype t) { return t == KDA_DTYPE_BF16 ? 2 : 4; }
+
+kda_status check_norm(const kda_residual_norm_args *a) {
+    if (!a || a->rows < 0 || a->D < 8 || a->D % 8 || !known_dtype(a->dtype) || !known_dtype(a->res_dtype)) return KDA_ERR_INVALID_ARG;
+    if (!(a->eps > 0.f)) return KDA_ERR_INVALID_ARG;
+    if (a->D > KDA_MAX_NORM_CHANNELS || a->rows > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (a->res_dtype != a->dtype && a->res_dtype != KDA_DTYPE_F32) return KDA_ERR_UNSUPPORTED;
+    if (a->rows > 0 && !a->y) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(a->y, a->r, a->gate, a->w_post, a->scale, a->w_pre)) return KDA_ERR_MISALIGNED;
+    return KDA_OK;
+}
+kda::NormArgs norm_args(const kda_residual_norm_args *p) {
+    kda::NormArgs a{};
+    a.y = p->y; a.r = p->r; a.gate = p->gate;
+    a.w_post = p->w_post; a.scale = p->scale; a.w_pre = p->w_pre;
+    a.res_scale = p->res_scale; a.eps = p->eps;
+    a.rows = p->rows; a.D = p->D;
+    a.res_bf16 = p->res_dtype == KDA_DTYPE_BF16;
+    return a;
+}
+
 kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
 }  // namespace
@@ -122,6 +167,86 @@ kda_status kda_ssm_backward(const void *x, const void *dt, const void *B, const 
     g.dA = o.dA; g.dD = o.dD; g.ddt_bias = o.ddt_bias; g.dS0 = o.dS0;
     g.ws = workspace;
     return done(kda::ssm_backward(g, dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_short_conv_swish_ex(const void *x, void *y, const kda_short_conv *conv, const float *bias,
+                                   const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t channels,
+                                   kda_dtype dtype, kda_stream_t stream) {
+    if (kda_status rc = check_conv(conv, bias, num_seqs, total_tokens, channels, dtype); rc != KDA_OK) return rc;
+    if (!cu_seqlens && num_seqs != 1) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!x || !y)) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(x, y, cu_seqlens)) return KDA_ERR_MISALIGNED;
+    if (total_tokens > 0 && overlap(x, y, (size_t)total_tokens * channels * size_of(dtype))) return KDA_ERR_INVALID_ARG;
+    return done(kda::conv_bias(conv_args(x, y, conv, bias, cu_seqlens, num_seqs, total_tokens, channels),
+                               dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_short_conv_step(const void *x, void *y, const kda_short_conv *conv, const float *bias, int32_t N,
+                               int32_t channels, kda_dtype dtype, kda_stream_t stream) {
+    if (N < 1) return KDA_ERR_INVALID_ARG;
+    if (kda_status rc = check_conv(conv, bias, 1, N, channels, dtype); rc != KDA_OK) return rc;
+    if (!x || !y || (conv->width > 1 && !conv->state_out)) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(x, y)) return KDA_ERR_MISALIGNED;
+    if (overlap(x, y, (size_t)N * channels * size_of(dtype))) return KDA_ERR_INVALID_ARG;
+    return done(kda::conv_step(conv_args(x, y, conv, bias, nullptr, N, N, channels), dtype == KDA_DTYPE_BF16,
+                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_short_conv_backward_workspace_size(int64_t total_tokens, int32_t channels, int32_t width) {
+    if (total_tokens < 0 || channels < 8 || channels % 8 || width < 1 || width > KDA_MAX_CONV_WIDTH) return 0;
+    return kda::conv_backward_workspace(total_tokens, channels, width);
+}
+
+kda_status kda_short_conv_backward(const void *x, const kda_short_conv *conv, const float *bias,
+                                   const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t channels,
+                                   kda_dtype dtype, const void *dy, kda_dtype dy_dtype, float *dx, float *dweight,
+                                   float *dbias, float *dstate, void *workspace, size_t workspace_bytes,
+                                   kda_stream_t stream) {
+    if (kda_status rc = check_conv(conv, bias, num_seqs, total_tokens, channels, dtype); rc != KDA_OK) return rc;
+    if (!cu_seqlens && num_seqs != 1) return KDA_ERR_INVALID_ARG;
+    if (!known_dtype(dy_dtype) || !dweight || (total_tokens > 0 && (!x || !dy || !dx))) return KDA_ERR_INVALID_ARG;
+    if (dy_dtype != dtype && dy_dtype != KDA_DTYPE_F32) return KDA_ERR_UNSUPPORTED;
+    const size_t need = kda::conv_backward_workspace(total_tokens, channels, conv->width);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+    if (!aligned16(x, dy, dx, dstate, workspace, cu_seqlens) || !aligned4(dweight, dbias)) return KDA_ERR_MISALIGNED;
+    kda::ConvBackwardArgs p{};
+    p.f = conv_args(x, nullptr, conv, bias, cu_seqlens, num_seqs, total_tokens, channels);
+    p.dy = dy; p.dy_bf16 = dy_dtype == KDA_DTYPE_BF16;
+    p.dx = dx; p.dw = dweight; p.dbias = dbias; p.dstate = dstate; p.ws = workspace;
+    return done(kda::conv_backward(p, dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_residual_norm(const kda_residual_norm_args *args, void *x, void *r_out, kda_stream_t stream) {
+    if (kda_status rc = check_norm(args); rc != KDA_OK) return rc;
+    if ((x != nullptr) != (args->w_pre != nullptr) && args->rows > 0) return KDA_ERR_INVALID_ARG;
+    if (args->rows > 0 && !r_out) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(x, r_out)) return KDA_ERR_MISALIGNED;
+    kda::NormArgs a = norm_args(args);
+    a.x = x; a.r_out = r_out;
+    return done(kda::residual_norm(a, args->dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_residual_norm_backward_workspace_size(int64_t rows, int32_t D) {
+    if (rows < 0 || D < 8 || D % 8 || D > KDA_MAX_NORM_CHANNELS) return 0;
+    return kda::residual_norm_backward_workspace(rows, D);
+}
+
+kda_status kda_residual_norm_backward(const kda_residual_norm_args *args, const void *dx, const float *dr_out, float *dy,
+                                      float *dr, float *dgate, float *dw_post, float *dscale, float *dw_pre,
+                                      void *workspace, size_t workspace_bytes, kda_stream_t stream) {
+    if (kda_status rc = check_norm(args); rc != KDA_OK) return rc;
+    if (args->rows > 0 && (!dy || (dx != nullptr) != (args->w_pre != nullptr) ||
+                           (dgate != nullptr) != (args->gate != nullptr)))
+        return KDA_ERR_INVALID_ARG;
+    if ((dw_post && !args->w_post) || (dscale && !args->scale) || (dw_pre && !args->w_pre)) return KDA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kda::residual_norm_backward_workspace(args->rows, args->D)) return KDA_ERR_WORKSPACE;
+    if (!aligned16(dx, dr_out, dy, dr, dgate, dw_post, dscale, dw_pre, workspace)) return KDA_ERR_MISALIGNED;
+    kda::NormBackwardArgs p{};
+    p.f = norm_args(args);
+    p.dx = dx; p.dr_out = dr_out;
+    p.dy = dy; p.dr = dr; p.dgate = dgate; p.dw_post = dw_post; p.dscale = dscale; p.dw_pre = dw_pre;
+    p.ws = workspace;
+    return done(kda::residual_norm_backward(p, args->dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,369 @@
+// kda_residual_norm.cu -- what stands between two blocks of a layer stack, in one pass over the rows:
+//
+//     u = RMSNorm(y) w_post,   r' = a r + s sigmoid(g) u,   x = RMSNorm(r') w_pre
+//
+// (the norm after a block, its gate and residual scale, the residual stream, the norm before the next
+// block), and its gradients: with rs1 = 1 / rms(y), rs2 = 1 / rms(r'), and row means <.>,
+//
+//     d = dr' + rs2 (w_pre dx - rs2^2 r' <w_pre dx r'>),   dr = a d,          dw_pre = sum dx rs2 r'
+//     dscale = sum d sigmoid(g) u,   dg = d s u sigmoid(g) (1 - sigmoid(g)),  f = d s sigmoid(g)
+//     dw_post = sum f rs1 y,         dy = rs1 (w_post f - rs1^2 y <w_post f y>).
+//
+// Bound by memory: every row is read once and stays in registers through its two (three) row sums. A
+// CTA takes a row at a time, one vector of 8 channels per thread (two above 4096 channels), and loads the
+// next row before it works on the current one. The column sums of the backward stay in each thread's registers over all
+// of its CTA's rows; one partial row per CTA goes to the workspace and norm_sum_kernel adds them in order.
+#include "kda_layer.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kMaxThreads = 512;
+
+// Sums of N values over the CTA, the same in every thread. Two calls in a row use different `slot`s.
+template <int N> __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[2][kMaxThreads / 32], int slot) {
+    const int warps = blockDim.x / 32, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
+    if (warps == 1) return;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[slot][i][warp] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float t = lane < warps ? red[slot][i][lane] : 0.f;
+#pragma unroll
+        for (int m = kMaxThreads / 64; m > 0; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+        v[i] = __shfl_sync(0xffffffffu, t, 0);
+    }
+}
+
+__device__ __forceinline__ void load_weights(const float *w, int c, float (&v)[8], float none) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = none;
+    if (w) {
+        const float4 a = *reinterpret_cast<const float4 *>(w + c), b = *reinterpret_cast<const float4 *>(w + c + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+}
+
+// One row's inputs as loaded.
+template <typename T, typename R, int V> struct Row {
+    Pack8<T> y[V], g[V];
+    Pack8<R> r[V];
+    __device__ __forceinline__ void load(const NormArgs &a, int64_t row) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (threadIdx.x + k * blockDim.x) * 8;
+            y[k].zero(), g[k].zero(), r[k].zero();
+            if (c >= a.D || row >= a.rows) continue;
+            const size_t at = (size_t)row * a.D + c;
+            y[k].load_stream(static_cast<const T *>(a.y) + at);
+            if (a.gate) g[k].load_stream(static_cast<const T *>(a.gate) + at);
+            if (a.r) r[k].load_stream(static_cast<const R *>(a.r) + at);
+        }
+    }
+};
+
+template <typename T, typename R, int V>
+__global__ void __launch_bounds__(kMaxThreads)
+norm_kernel(const NormArgs a) {
+    __shared__ float red[2][2][kMaxThreads / 32];
+    const float inv = 1.f / a.D;
+    Row<T, R, V> next;
+    if (V == 1) next.load(a, blockIdx.x);  // (two vectors per thread leave no registers for a row ahead)
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        if (V > 1) next.load(a, row);
+        const Row<T, R, V> in = next;
+        if (V == 1) next.load(a, row + gridDim.x);
+        float out[V][8], sum[1] = {0.f};
+        if (a.w_post) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                float y[8];
+                in.y[k].get(y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[0] = fmaf(y[i], y[i], sum[0]);
+            }
+            row_sums(sum, red, 0);
+        }
+        const float rs1 = rsqrtf(fmaf(sum[0], inv, a.eps));
+        sum[0] = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (threadIdx.x + k * blockDim.x) * 8, cc = min(c, a.D - 8);
+            float y[8], g[8], r[8], w[8], s[8];
+            in.y[k].get(y);
+            in.r[k].get(r);
+            load_weights(a.scale, cc, s, 1.f);
+            if (a.w_post) {
+                load_weights(a.w_post, cc, w, 1.f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] *= rs1 * w[i];
+            }
+            if (a.gate) {
+                in.g[k].get(g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] *= sigmoid_f(g[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                out[k][i] = c < a.D ? fmaf(a.res_scale, r[i], s[i] * y[i]) : 0.f;
+                sum[0] = fmaf(out[k][i], out[k][i], sum[0]);
+            }
+            if (c < a.D) {
+                Pack8<R> o;
+                o.set(out[k]);
+                o.store_stream(static_cast<R *>(a.r_out) + (size_t)row * a.D + c);
+            }
+        }
+        if (!a.w_pre) {
+            if (a.w_post) __syncthreads();  // the next row's sum takes the slot that this row's readers may still read
+            continue;
+        }
+        row_sums(sum, red, 1);
+        const float rs2 = rsqrtf(fmaf(sum[0], inv, a.eps));
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (threadIdx.x + k * blockDim.x) * 8;
+            if (c >= a.D) continue;
+            float w[8], v[8];
+            load_weights(a.w_pre, c, w, 1.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = out[k][i] * rs2 * w[i];
+            Pack8<T> o;
+            o.set(v);
+            o.store_stream(static_cast<T *>(a.x) + (size_t)row * a.D + c);
+        }
+        // (without w_post the next row's sum takes the same slot: its writers have to wait for the readers)
+        if (!a.w_post) __syncthreads();
+    }
+}
+
+template <typename T, typename R, int V>
+__global__ void __launch_bounds__(kMaxThreads)
+norm_backward_kernel(const NormBackwardArgs p, float *__restrict__ part) {
+    const NormArgs &a = p.f;
+    __shared__ float red[3][2][kMaxThreads / 32];
+    const float inv = 1.f / a.D;
+    float d_post[V][8], d_scale[V][8], d_pre[V][8];
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d_post[k][i] = d_scale[k][i] = d_pre[k][i] = 0.f;
+    Row<T, R, V> next;
+    Pack8<T> ndx[V];
+    Pack8<float> ndr[V];
+    auto load = [&](int64_t row) {
+        next.load(a, row);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (threadIdx.x + k * blockDim.x) * 8;
+            ndx[k].zero(), ndr[k].zero();
+            if (c >= a.D || row >= a.rows) continue;
+            const size_t at = (size_t)row * a.D + c;
+            if (p.dx) ndx[k].load_stream(static_cast<const T *>(p.dx) + at);
+            if (p.dr_out) ndr[k].load_stream(p.dr_out + at);
+        }
+    };
+    if (V == 1) load(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        if (V > 1) load(row);
+        const Row<T, R, V> in = next;
+        float d[V][8], h[V][8];  // dr', w_pre dx
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            ndr[k].get(d[k]);
+            ndx[k].get(h[k]);
+        }
+        if (V == 1) load(row + gridDim.x);
+        float sum[1] = {0.f};
+        if (a.w_post) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                float y[8];
+                in.y[k].get(y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[0] = fmaf(y[i], y[i], sum[0]);
+            }
+            row_sums(sum, red, 0);
+        }
+        const float rs1 = rsqrtf(fmaf(sum[0], inv, a.eps));
+        float two[2] = {0.f, 0.f}, out[V][8];  // sums of r'^2 and w_pre dx r'
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (threadIdx.x + k * blockDim.x) * 8, cc = min(c, a.D - 8);
+            float y[8], g[8], r[8], w[8], s[8], q[8];
+            in.y[k].get(y);
+            in.g[k].get(g);
+            in.r[k].get(r);
+            load_weights(a.scale, cc, s, 1.f);
+            load_weights(a.w_post, cc, w, 1.f);
+            load_weights(a.w_pre, cc, q, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float u = y[i];
+                if (a.w_post) u *= rs1 * w[i];
+                if (a.gate) u *= sigmoid_f(g[i]);
+                out[k][i] = c < a.D ? fmaf(a.res_scale, r[i], s[i] * u) : 0.f;
+                two[0] = fmaf(out[k][i], out[k][i], two[0]);
+                two[1] = fmaf(h[k][i] * q[i], out[k][i], two[1]);
+            }
+        }
+        float rs2 = 0.f, mean = 0.f;
+        if (a.w_pre) {
+            row_sums(two, red, 1);
+            rs2 = rsqrtf(fmaf(two[0], inv, a.eps));
+            mean = two[1] * inv * rs2 * rs2;
+        }
+        sum[0] = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (threadIdx.x + k * blockDim.x) * 8, cc = min(c, a.D - 8);
+            const bool on = c < a.D;
+            const size_t at = (size_t)row * a.D + c;
+            float y[8], g[8], w[8], s[8], q[8], o[8];
+            in.y[k].get(y);
+            in.g[k].get(g);
+            load_weights(a.scale, cc, s, 1.f);
+            load_weights(a.w_post, cc, w, 1.f);
+            load_weights(a.w_pre, cc, q, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                d_pre[k][i] = fmaf(h[k][i], out[k][i] * rs2, d_pre[k][i]);
+                d[k][i] = fmaf(rs2, fmaf(-out[k][i], mean, h[k][i] * q[i]), d[k][i]);
+                o[i] = a.res_scale * d[k][i];
+            }
+            Pack8<float> v;
+            if (on && p.dr) {
+                v.set(o);
+                v.store_stream(p.dr + at);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float u = a.w_post ? y[i] * rs1 * w[i] : y[i];
+                const float m = a.gate ? sigmoid_f(g[i]) : 1.f;
+                d_scale[k][i] = fmaf(d[k][i], m * u, d_scale[k][i]);
+                const float ds = d[k][i] * s[i];
+                o[i] = ds * u * m * (1.f - m);
+                const float f = ds * m;
+                d_post[k][i] = fmaf(f, y[i] * rs1, d_post[k][i]);
+                d[k][i] = a.w_post ? f * w[i] : f;  // w_post f
+                sum[0] = fmaf(d[k][i], y[i], sum[0]);
+            }
+            if (on && a.gate) {
+                v.set(o);
+                v.store_stream(p.dgate + at);
+            }
+        }
+        float back = 0.f;
+        if (a.w_post) {
+            row_sums(sum, red, 2);
+            back = sum[0] * inv * rs1 * rs1;
+        } else {
+            __syncthreads();  // the next row's sum takes the slot that this row's readers may still read
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (threadIdx.x + k * blockDim.x) * 8;
+            if (c >= a.D) continue;
+            float y[8], o[8];
+            in.y[k].get(y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = a.w_post ? rs1 * fmaf(-y[i], back, d[k][i]) : d[k][i];
+            Pack8<float> v;
+            v.set(o);
+            v.store_stream(p.dy + (size_t)row * a.D + c);
+        }
+    }
+    // this CTA's column sums: [w_post | scale | w_pre]
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int c = (threadIdx.x + k * blockDim.x) * 8;
+        if (c >= a.D) continue;
+        float *to = part + (size_t)blockIdx.x * 3 * a.D + c;
+        Pack8<float> v;
+        v.set(d_post[k]);
+        v.store(to);
+        v.set(d_scale[k]);
+        v.store(to + a.D);
+        v.set(d_pre[k]);
+        v.store(to + 2 * a.D);
+    }
+}
+
+// Column sums: the CTAs' partial rows, added by kLanes threads per column and then over those, in order.
+constexpr int kLanes = 8;
+__global__ void __launch_bounds__(256)
+norm_sum_kernel(const float *__restrict__ part, const int n, const int D, float *__restrict__ d0, float *__restrict__ d1,
+                float *__restrict__ d2) {
+    __shared__ float red[kLanes][32];
+    const int c = blockIdx.x * 32 + threadIdx.x % 32, lane = threadIdx.x / 32, j = blockIdx.y;
+    float *to = j == 0 ? d0 : j == 1 ? d1 : d2;
+    if (!to) return;
+    float v = 0.f;
+    if (c < D) {
+#pragma unroll 4
+        for (int r = lane; r < n; r += kLanes) v += part[((size_t)r * 3 + j) * D + c];
+    }
+    red[lane][threadIdx.x % 32] = v;
+    __syncthreads();
+    if (lane || c >= D) return;
+#pragma unroll
+    for (int k = 1; k < kLanes; ++k) v += red[k][threadIdx.x];
+    to[c] = v;
+}
+
+int threads_of(int D) {  // one vector of 8 channels per thread, up to kMaxThreads
+    return min(kMaxThreads, (D / 8 + 31) / 32 * 32);
+}
+// CTAs: enough rows in flight on every SM (a row of 512 threads, or several of fewer).
+int64_t ctas_of(int64_t rows, int D, int per_sm) {
+    return max((int64_t)1, min(rows, (int64_t)148 * per_sm * (kMaxThreads / threads_of(D))));
+}
+constexpr int kBackPerSm = 1;
+
+template <typename T, typename R> cudaError_t launch(const NormArgs &a, cudaStream_t st) {
+    const int nt = threads_of(a.D), V = (a.D / 8 + nt - 1) / nt;
+    if (a.rows == 0) return cudaSuccess;
+    const unsigned grid = (unsigned)ctas_of(a.rows, a.D, 2);
+    if (V == 1) norm_kernel<T, R, 1><<<grid, nt, 0, st>>>(a);
+    else norm_kernel<T, R, 2><<<grid, nt, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, typename R> cudaError_t launch_back(const NormBackwardArgs &p, cudaStream_t st) {
+    const NormArgs &a = p.f;
+    const int nt = threads_of(a.D), V = (a.D / 8 + nt - 1) / nt;
+    const unsigned grid = (unsigned)ctas_of(a.rows, a.D, kBackPerSm);
+    float *part = static_cast<float *>(p.ws);
+    if (V == 1) norm_backward_kernel<T, R, 1><<<grid, nt, 0, st>>>(p, part);
+    else norm_backward_kernel<T, R, 2><<<grid, nt, 0, st>>>(p, part);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (p.dw_post || p.dscale || p.dw_pre)
+        norm_sum_kernel<<<dim3((a.D + 31) / 32, 3), 256, 0, st>>>(part, (int)grid, a.D, p.dw_post, p.dscale, p.dw_pre);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t residual_norm(const NormArgs &a, bool bf16, cudaStream_t st) {
+    if (!bf16) return launch<float, float>(a, st);
+    return a.res_bf16 ? launch<__nv_bfloat16, __nv_bfloat16>(a, st) : launch<__nv_bfloat16, float>(a, st);
+}
+
+size_t residual_norm_backward_workspace(int64_t rows, int D) {
+    return (size_t)ctas_of(rows, D, kBackPerSm) * 3 * D * sizeof(float);
+}
+
+cudaError_t residual_norm_backward(const NormBackwardArgs &p, bool bf16, cudaStream_t st) {
+    if (!bf16) return launch_back<float, float>(p, st);
+    return p.f.res_bf16 ? launch_back<__nv_bfloat16, __nv_bfloat16>(p, st) : launch_back<__nv_bfloat16, float>(p, st);
+}
+
+}  // namespace kda

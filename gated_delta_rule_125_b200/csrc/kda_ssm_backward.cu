@@ -27,6 +27,30 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 
+// 2^x for two x, more exactly than the hardware's near x = 0: x = i + r, 2^r = 1 + r q(r) with q the
+// polynomial of degree 4 that interpolates (2^r - 1) / r at the five Chebyshev points of [-1/2, 1/2]
+// (error below 2.1e-7 of the result, and of x itself for small x: a slow decay keeps its rate over a
+// long chain). Adding 1.5 2^23 rounds x to the integer i in the low bits. The gradients' own chain
+// takes this one: with the hardware's exponential the gradient of S0 after 500 tokens was off by 1.0e-6
+// of its norm, with this one by 4e-7, what rounding the chain leaves.
+__device__ __forceinline__ F2 exp2_poly2(F2 x) {
+    float a, b;
+    unpack(x, a, b);
+    x = f2(fminf(fmaxf(a, -126.f), 127.f), fminf(fmaxf(b, -126.f), 127.f));
+    const F2 t = add2(x, f2(12582912.f, 12582912.f)), i = add2(t, f2(-12582912.f, -12582912.f));
+    const F2 r = fma2(i, f2(-1.f, -1.f), x);
+    F2 q = fma2(r, f2(0.00133813021f, 0.00133813021f), f2(0.00966636837f, 0.00966636837f));
+    q = fma2(r, q, f2(0.0555038117f, 0.0555038117f));
+    q = fma2(r, q, f2(0.240223497f, 0.240223497f));
+    q = fma2(r, q, f2(0.693147182f, 0.693147182f));
+    q = fma2(r, q, f2(1.f, 1.f));
+    float t0, t1, q0, q1;
+    unpack(t, t0, t1);
+    unpack(q, q0, q1);
+    return f2(__int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23)),
+              __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23)));
+}
+
 template <int NS, int LPC> struct BackMem {
     static constexpr int N_ = NS * LPC, CB = kThreads / LPC;
     static constexpr int UG = 16 / NS;                       // tokens of a group: 16 (token, state) values per lane
@@ -218,7 +242,7 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
                         const float2 m = *reinterpret_cast<const float2 *>(sm.sBC + (v + u) * 2 * N_ + (p * LPC + q) * 4);
-                        av[u][p] = exp2_pair(mul2(f2(w[u].x, w[u].x), A2[p]));
+                        av[u][p] = exp2_poly2(mul2(f2(w[u].x, w[u].x), A2[p]));
                         bv[u][p] = mul2(f2(w[u].y, w[u].y), f2(m.x, m.y));
                     }
                 }

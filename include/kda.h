@@ -471,6 +471,88 @@ kda_status kda_ssm_backward(const void *x, const void *dt, const void *B, const 
                             const kda_ssm_grads *grads, void *workspace, size_t workspace_bytes,
                             kda_stream_t stream);
 
+/*
+ * kda_short_conv_swish with a bias: y_t[c] = v sigmoid(v), v = bias[c] + z_t[c] (z as above); bias [C]
+ * fp32, 4-byte aligned (NULL: none, then the same values as kda_short_conv_swish to rounding). Rows
+ * from cu_seqlens[N] on are neither read nor written. Launches as kda_short_conv_launches().
+ */
+kda_status kda_short_conv_swish_ex(const void *x, void *y, const kda_short_conv *conv, const float *bias,
+                                   const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                   int32_t channels, kda_dtype dtype, kda_stream_t stream);
+
+/*
+ * One token of each of N sequences: x, y [N][C], conv->state_out [N][W-1][C] read and shifted in place
+ * (conv->state_in is not used; W = 1 needs no state). bias [C] fp32 or NULL. Windows 1 ..
+ * KDA_MAX_CONV_WIDTH. y must not overlap x. One launch.
+ */
+kda_status kda_short_conv_step(const void *x, void *y, const kda_short_conv *conv, const float *bias, int32_t N,
+                               int32_t channels, kda_dtype dtype, kda_stream_t stream);
+
+/*
+ * Gradients of a loss through y of kda_short_conv_swish(_ex), given dy = dL/dy [T][C]: fp32 (as
+ * kda_backward gives it), or in the io dtype with dy_dtype = dtype. state_out is not differentiated
+ * (it holds raw inputs). conv->state_in as in the forward call; conv->state_out is not used.
+ *
+ *   dx [T][C], dweight [C][W] fp32; dbias [C] fp32 or NULL (not written); dstate [N][W-1][C] fp32 (the
+ *   gradient of state_in) or NULL (not written). dx, dstate and workspace 16-byte aligned.
+ *
+ * Rows from cu_seqlens[N] on are neither read nor written. dweight and dbias are summed in a fixed
+ * order (no atomics). workspace: kda_short_conv_backward_workspace_size() bytes (a partial dweight and
+ * dbias per 64 tokens). Two launches, three with dstate and cu_seqlens.
+ */
+size_t kda_short_conv_backward_workspace_size(int64_t total_tokens, int32_t channels, int32_t width);
+kda_status kda_short_conv_backward(const void *x, const kda_short_conv *conv, const float *bias,
+                                   const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                   int32_t channels, kda_dtype dtype, const void *dy, kda_dtype dy_dtype,
+                                   float *dx, float *dweight, float *dbias, float *dstate, void *workspace,
+                                   size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * What stands between two blocks of a layer stack, in one pass: the norm after a block, its gate and
+ * residual scale, the residual stream, the norm before the next block. Per row t of D channels,
+ *
+ *     u = y rsqrt(mean(y^2) + eps) w_post          (w_post NULL: u = y)
+ *     r_out = res_scale r + scale sigmoid(gate) u  (each of r, scale, gate may be NULL: 0, 1, 1)
+ *     x = r_out rsqrt(mean(r_out^2) + eps) w_pre   (w_pre and x NULL: not computed)
+ *
+ *   y, gate, x  [rows][D] dtype          r, r_out  [rows][D] res_dtype (dtype, or fp32)
+ *   w_post, scale, w_pre  [D] fp32       D a multiple of 8, at most KDA_MAX_NORM_CHANNELS
+ *
+ * All 16-byte aligned. x is computed from r_out before its rounding. r_out may be r; no other output may
+ * overlap an input. Arithmetic is fp32. One launch.
+ */
+#define KDA_MAX_NORM_CHANNELS 8192
+typedef struct kda_residual_norm_args {
+    const void *y;
+    const void *r;
+    const void *gate;
+    const float *w_post;
+    const float *scale;
+    const float *w_pre;
+    float res_scale;
+    float eps;
+    int64_t rows;
+    int32_t D;
+    kda_dtype dtype;
+    kda_dtype res_dtype;
+} kda_residual_norm_args;
+kda_status kda_residual_norm(const kda_residual_norm_args *args, void *x, void *r_out, kda_stream_t stream);
+
+/*
+ * Gradients of a loss through x and r_out, given dx = dL/dx [rows][D] dtype (NULL iff w_pre is) and
+ * dr_out = dL/dr_out [rows][D] fp32 (or NULL: zero). The forward's inputs are read again (r as it was
+ * before the call). All gradients are fp32: dy [rows][D]; dr [rows][D] or NULL (not written); dgate
+ * [rows][D] (NULL iff gate is); dw_post, dscale, dw_pre [D] or NULL (not written; NULL where the weight
+ * is). dr may be dr_out; no other output may overlap an input. All 16-byte aligned. Column sums are
+ * added in a fixed order (no atomics). workspace: kda_residual_norm_backward_workspace_size() bytes.
+ * Two launches.
+ */
+size_t kda_residual_norm_backward_workspace_size(int64_t rows, int32_t D);
+kda_status kda_residual_norm_backward(const kda_residual_norm_args *args, const void *dx, const float *dr_out,
+                                      float *dy, float *dr, float *dgate, float *dw_post, float *dscale,
+                                      float *dw_pre, void *workspace, size_t workspace_bytes,
+                                      kda_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -413,3 +413,300 @@ def test_ssm_backward_graph():
     ref = ssm_grad_run(k, dy, dS)
     for u, v in zip(out, ref):
         assert torch.equal(u, v)
+
+
+# ----------------------------------------------------------- short convolution ----
+# A sum of W products and a bias: (W + 1) 2^-24 of its terms' magnitude, through a Swish whose slope is at
+# most 1.1, its exponential and reciprocal good to 2^-22 each: chain 4 W + 16 steps of 2^-21 covers it. dw
+# and dbias add T terms (at most T 2^-24, 64 in a row and then the runs).
+
+def conv_case(lengths, C, W, dtype, bias=True, state=True, seed=0):
+    T, N = sum(lengths), len(lengths)
+    return dict(x=randn(T, C, seed=seed + 1, dtype=dtype), w=randn(C, W, seed=seed + 2, std=W ** -0.5), cu=cu_of(lengths),
+                bias=randn(C, seed=seed + 3) if bias else None,
+                state=randn(N, W - 1, C, seed=seed + 4, dtype=dtype) if state else None)
+
+
+def conv_check(k, y, last, lengths):
+    h = {n: (None if v is None else v.cpu().numpy() if n == "cu" else host(v)) for n, v in k.items()}
+    ref, last_ref = L.conv(h["x"], h["w"], h["cu"], h["state"], h["bias"])
+    a = {n: None if v is None or n == "cu" else np.abs(v) for n, v in h.items()}
+    rows = np.zeros_like(ref)
+    W = h["w"].shape[1]
+    for s, b, e, r in L._windows(a["x"], W, h["cu"], a["state"]):
+        rows[b:e] = sum(a["w"][:, j] * r[j:j + e - b] for j in range(W)) + (0 if a["bias"] is None else a["bias"])
+    within(y, ref, 1.1 * rows, 4 * W + 16, "y")
+    if last is not None:
+        np.testing.assert_array_equal(host(last), last_ref)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lengths,C,W", [([1], 8, 4), ([100], 72, 4), ([0, 5, 1, 0, 17, 16, 2, 0], 24, 4), ([33, 20], 16, 1),
+                                         ([1] * 40, 16, 8), ([50, 3], 8, 8), ([40, 9], 40, 5), ([16, 33], 16, 2), ([31], 8, 3)])
+def test_conv_bias(lengths, C, W, dtype):
+    k = conv_case(lengths, C, W, dtype, seed=W)
+    last = torch.empty_like(k["state"])
+    y = kda.kda_short_conv_swish(k["x"], k["w"], k["cu"], state_in=k["state"], state_out=last, bias=k["bias"], y=nan_like(k["x"]))
+    conv_check(k, y, last, lengths)
+    y = kda.kda_short_conv_swish(k["x"], k["w"], k["cu"], bias=k["bias"])
+    conv_check(dict(k, state=None), y, None, lengths)
+    # the state in place
+    st = k["state"].clone()
+    kda.kda_short_conv_swish(k["x"], k["w"], k["cu"], state_in=st, state_out=st, bias=k["bias"])
+    assert torch.equal(st, last)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,C,W", [(1, 8, 4), (5, 4096, 4), (300, 40, 4), (3, 16, 1), (4, 24, 8), (2, 8, 2)])
+def test_conv_step(N, C, W, dtype):
+    k = conv_case([1] * N, C, W, dtype, seed=N)
+    st = k["state"].clone()
+    y = kda.kda_short_conv_step(k["x"], k["w"], st if W > 1 else None, bias=k["bias"])
+    conv_check(k, y, st, [1] * N)
+    st = k["state"].clone()
+    conv_check(dict(k, bias=None), kda.kda_short_conv_step(k["x"], k["w"], st), st, [1] * N)
+
+
+def test_conv_steps_continue_a_prompt():
+    k = conv_case([20], 64, 4, BF16, seed=5)
+    last = torch.empty_like(k["state"])
+    y = kda.kda_short_conv_swish(k["x"], k["w"], state_in=k["state"], state_out=last, bias=k["bias"])
+    st = torch.empty_like(last)
+    out = [kda.kda_short_conv_swish(k["x"][:15].clone(), k["w"], state_in=k["state"], state_out=st, bias=k["bias"])]
+    out += [kda.kda_short_conv_step(k["x"][t:t + 1].clone(), k["w"], st, bias=k["bias"]) for t in range(15, 20)]
+    assert torch.equal(torch.cat(out), y) and torch.equal(st, last)
+
+
+@pytest.mark.parametrize("dtype,dy_dtype", [(F32, F32), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("lengths,C,W", [([1], 8, 4), ([64], 16, 4), ([65], 16, 4), ([0, 5, 1, 0, 64, 2, 63, 130, 0], 24, 4), ([70, 3], 8, 1),
+                                         ([1] * 70, 16, 8), ([62, 4, 200], 8, 8), ([67], 8, 5), ([66, 66], 72, 2), ([63, 1, 3], 8, 3)])
+def test_conv_backward(lengths, C, W, dtype, dy_dtype):
+    k = conv_case(lengths, C, W, dtype, seed=W + 1)
+    T = sum(lengths)
+    dy = randn(T, C, seed=9, dtype=dy_dtype)
+    h = {n: (v.cpu().numpy() if n == "cu" else host(v)) for n, v in k.items()}
+    for state in (True, False):
+        got = kda.kda_short_conv_backward(k["x"], k["w"], dy, k["cu"], bias=k["bias"], state_in=k["state"] if state else None,
+                                          want_dstate=True)
+        st = h["state"] if state else None
+        ref = L.conv_backward(h["x"], h["w"], host(dy), h["cu"], st, h["bias"])
+        # magnitudes: every product of the gradient of v (at most 1.1 |dy| and its own error, that of v, 4 W + 16 steps
+        # of its terms) with a tap or a row
+        v = np.abs(L.conv(np.abs(h["x"]), np.abs(h["w"]), h["cu"], None if st is None else np.abs(st), np.abs(h["bias"]))[0]) + 1
+        g = 1.1 * np.abs(host(dy)) * (2 + 2 * v)
+        mdx, mdw, mdb, mds = np.zeros_like(h["x"]), np.zeros_like(h["w"]), g.sum(0), np.zeros((len(lengths), W - 1, C))
+        for s, b, e, rows in L._windows(np.abs(h["x"]), W, h["cu"], None if st is None else np.abs(st)):
+            d = np.zeros_like(rows)
+            for j in range(W):
+                d[j:j + e - b] += g[b:e] * np.abs(h["w"][:, j])
+                mdw[:, j] += (g[b:e] * rows[j:j + e - b]).sum(0)
+            mdx[b:e], mds[s] = d[W - 1:], d[:W - 1]
+        chain = 4 * W + 16
+        for n, a, r, m in zip(("dx", "dw", "dbias", "dstate"), got, ref, (mdx, mdw, mdb, mds)):
+            within(a, r, m, chain + (T / 8 if n in ("dw", "dbias") else 0), n)
+    # without the optional outputs the rest keeps its bits
+    again = kda.kda_short_conv_backward(k["x"], k["w"], dy, k["cu"], bias=k["bias"])
+    assert all(torch.equal(a, b) for a, b in zip(again[:3], got[:3])) and again[3] is None
+    again = kda.kda_short_conv_backward(k["x"], k["w"], dy, k["cu"])
+    assert again[2] is None
+    within(again[0], L.conv_backward(h["x"], h["w"], host(dy), h["cu"])[0], mdx, chain, "dx without bias")
+
+
+def test_conv_rows_behind_the_last_sequence():
+    k = conv_case([50, 20], 16, 4, F32, seed=6)
+    x = torch.cat([k["x"], torch.full((130, 16), float("nan"), device=DEV)])
+    dy = torch.cat([randn(70, 16, seed=7), torch.full((130, 16), float("nan"), device=DEV)])
+    y = torch.full_like(x, 7.0)
+    kda.kda_short_conv_swish(x, k["w"], k["cu"], bias=k["bias"], y=y)
+    assert (y[70:] == 7.0).all() and torch.equal(y[:70], kda.kda_short_conv_swish(k["x"], k["w"], k["cu"], bias=k["bias"]))
+    a = kda.kda_short_conv_backward(x, k["w"], dy, k["cu"], bias=k["bias"])
+    b = kda.kda_short_conv_backward(k["x"], k["w"], dy[:70].clone(), k["cu"], bias=k["bias"])
+    assert torch.equal(a[0][:70], b[0])
+    for u, v in zip(a[1:3], b[1:3]):
+        assert torch.equal(u, v)
+
+
+# -------------------------------------------------------------- residual norms ----
+# Row sums of D terms by a tree of at most 8 + log2(512) + 9 additions; everything else a few operations on the
+# element: chain 64 covers it. Column sums add rows (at most rows / 8 + 8 in a row).
+
+def norm_case(rows, D, dtype, res, post=True, gate=True, scale=True, pre=True, stream=True, seed=0):
+    pick = lambda has, *a, **k: randn(*a, **k) if has else None
+    return dict(y=randn(rows, D, seed=seed + 1, dtype=dtype), r=pick(stream, rows, D, seed=seed + 2, std=2.0, dtype=res),
+                w_pre=pick(pre, D, seed=seed + 3, mean=1.0, std=0.3), w_post=pick(post, D, seed=seed + 4, mean=1.0, std=0.3),
+                gate=pick(gate, rows, D, seed=seed + 5, dtype=dtype), scale=pick(scale, D, seed=seed + 6))
+
+
+def norm_call(k, **kw):
+    return kda.kda_residual_norm(k["y"], k["r"], k["w_pre"], w_post=k["w_post"], gate=k["gate"], scale=k["scale"],
+                                 res_scale=0.75, eps=1e-5, **kw)
+
+
+NORM_OPTIONS = [(1, 1, 1, 1, 1), (0, 0, 0, 1, 1), (1, 0, 0, 0, 1), (0, 1, 1, 1, 0), (0, 0, 0, 0, 1), (1, 1, 0, 1, 1)]
+
+
+def norm_mags(h):
+    """|terms| of r' and of x: x divides by the row's rms, whose own relative error is that of a sum of squares."""
+    u = np.abs(L.norm(h["y"], None, None, h["w_post"], h["gate"], h["scale"], 0.75, 1e-5)[1])
+    out = u + (0 if h["r"] is None else 0.75 * np.abs(h["r"]))
+    return out
+
+
+@pytest.mark.parametrize("dtype,res", [(F32, F32), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("rows,D", [(1, 8), (3, 264), (5, 4096), (700, 128), (4, 8192), (9, 5000), (2, 4104), (1, 1024)])
+def test_residual_norm(rows, D, dtype, res):
+    for opt in NORM_OPTIONS:
+        post, gate, scale, pre, stream = opt
+        k = norm_case(rows, D, dtype, res if stream else dtype, post, gate, scale, pre, stream, seed=D)
+        x, r = norm_call(k)
+        h = {n: host(v) for n, v in k.items()}
+        x_ref, r_ref = L.norm(**h, res_scale=0.75, eps=1e-5)
+        mag = norm_mags(h)
+        within(r, r_ref, mag, 64, "r' %s" % (opt,))
+        if pre:
+            rms = np.sqrt((r_ref ** 2).mean(-1, keepdims=True) + 1e-5)
+            within(x, x_ref, mag / rms * np.abs(h["w_pre"]) * (1 + (mag * np.abs(r_ref)).mean(-1, keepdims=True) / rms ** 2), 64, "x %s" % (opt,))
+        else:
+            assert x is None
+        if stream:  # the stream in place
+            keep = k["r"].clone()
+            norm_call(k, r_out=k["r"])
+            assert torch.equal(k["r"], r)
+            k["r"] = keep
+
+
+@pytest.mark.parametrize("dtype,res", [(F32, F32), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("rows,D", [(1, 8), (3, 264), (300, 4096), (1500, 128), (4, 8192), (9, 5000), (2, 4104)])
+def test_residual_norm_backward(rows, D, dtype, res):
+    for opt in NORM_OPTIONS:
+        post, gate, scale, pre, stream = opt
+        k = norm_case(rows, D, dtype, res if stream else dtype, post, gate, scale, pre, stream, seed=D + 1)
+        dx = randn(rows, D, seed=31, dtype=dtype) if pre else None
+        for dr in (randn(rows, D, seed=32), None):
+            if dr is None and not pre:
+                continue
+            g = kda.kda_residual_norm_backward(k["y"], k["r"], k["w_pre"], dx, dr, w_post=k["w_post"], gate=k["gate"],
+                                               scale=k["scale"], res_scale=0.75, eps=1e-5)
+            h = {n: host(v) for n, v in k.items()}
+            ref = L.norm_backward(dx=host(dx), dr=host(dr), **h, res_scale=0.75, eps=1e-5)
+            mag = norm_grad_mags(h, host(dx), host(dr))
+            for n in ("dy", "dr", "dgate", "dw_post", "dscale", "dw_pre"):
+                got = getattr(g, n)
+                if got is None:
+                    assert (k if n != "dy" else h)[n[1:]] is None
+                    continue
+                within(got, ref[n], mag[n], 64 + (rows / 8 if n in ("dw_post", "dscale", "dw_pre") else 0), "%s %s" % (n, opt))
+
+
+def norm_grad_mags(h, dx, dr):
+    """norm_backward with every term taken positive, its row factors as they are; a row's 1 / rms enters each
+    twice, with the relative error of its sum."""
+    out = L.norm(**h, res_scale=0.75, eps=1e-5)[1]
+    om = norm_mags(h)
+    d = np.zeros_like(out) if dr is None else np.abs(dr)
+    m = {}
+    amp = 1.0
+    if h["w_pre"] is not None:
+        rs = 1 / np.sqrt((out ** 2).mean(-1, keepdims=True) + 1e-5)
+        amp = 2 + 2 * (om * np.abs(out)).mean(-1, keepdims=True) * rs ** 2
+        m["dw_pre"] = (np.abs(dx) * om * rs * amp).sum(0)
+        dh = np.abs(dx * h["w_pre"])
+        d = d + rs * amp * (dh + om * rs * (dh * om * rs).mean(-1, keepdims=True))
+    m["dr"] = 0.75 * d
+    rs = None if h["w_post"] is None else 1 / np.sqrt((h["y"] ** 2).mean(-1, keepdims=True) + 1e-5)
+    u = np.abs(h["y"] if rs is None else h["y"] * rs * h["w_post"])
+    s = 1.0 if h["gate"] is None else L.sigmoid(h["gate"])
+    m["dscale"] = 2 * (d * s * u).sum(0)
+    d = d if h["scale"] is None else d * np.abs(h["scale"])
+    if h["gate"] is not None:
+        m["dgate"] = 4 * d * u * s
+        d = d * s
+    if rs is not None:
+        hat = np.abs(h["y"] * rs)
+        m["dw_post"] = 2 * (d * hat).sum(0)
+        dh = d * np.abs(h["w_post"])
+        d = 2 * rs * (dh + hat * (dh * hat).mean(-1, keepdims=True))
+    m["dy"] = d
+    return m
+
+
+def test_residual_norm_many_rows_same_bits():
+    """More rows than CTAs; the column sums give the same bits each time; zero rows."""
+    k = norm_case(5000, 512, BF16, F32, seed=3)
+    dx, dr = randn(5000, 512, seed=4, dtype=BF16), randn(5000, 512, seed=5)
+    run = lambda kk, a, b: kda.kda_residual_norm_backward(kk["y"], kk["r"], kk["w_pre"], a, b, w_post=kk["w_post"], gate=kk["gate"],
+                                                          scale=kk["scale"], res_scale=0.75, eps=1e-5)
+    a, b = run(k, dx, dr), run(k, dx, dr)
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
+    h = {n: host(v) for n, v in k.items()}
+    ref = L.norm_backward(dx=host(dx), dr=host(dr), **h, res_scale=0.75, eps=1e-5)
+    mag = norm_grad_mags(h, host(dx), host(dr))
+    for n in ("dw_post", "dscale", "dw_pre"):
+        within(getattr(a, n), ref[n], mag[n], 64 + 5000 / 8, n)
+    none = {n: (v[:0] if v is not None and v.dim() == 2 else v) for n, v in k.items()}
+    assert norm_call(none)[0].shape == (0, 512)
+    g = run(none, dx[:0], dr[:0])
+    assert (g.dw_pre == 0).all() and (g.dscale == 0).all()
+
+
+def test_layer_together():
+    """A block as it is used: norm before, convolution, scan, norm after with gate and residual, forwards and
+    backwards, every call's outputs the next one's inputs; on a side stream and in a graph the same bits."""
+    lengths, C, n = [150, 60, 1], 64, 16
+    T, cu = sum(lengths), cu_of(lengths)
+    ssm = ssm_case(lengths, C, n, 1, BF16, seed=60)
+    conv = conv_case(lengths, C, 4, BF16, seed=61)
+    nk = norm_case(T, C, BF16, F32, seed=62)
+    y0, dx_out = randn(T, C, seed=63, dtype=BF16), randn(T, C, seed=64, dtype=BF16)
+
+    def block():
+        p = dict(w_post=nk["w_post"], gate=nk["gate"], scale=nk["scale"], res_scale=0.75, eps=1e-5)
+        x, r = kda.kda_residual_norm(y0, nk["r"], nk["w_pre"], **p)
+        u = kda.kda_short_conv_swish(x, conv["w"], cu, state_in=conv["state"], bias=conv["bias"])
+        sp = dict(D=ssm["D"], dt_bias=ssm["dt_bias"], z=ssm["z"])
+        y, S, tiles = kda.kda_ssm_prefill(u, ssm["dt"], ssm["B"], ssm["C"], ssm["A"], ssm["S0"], cu, save_states=True, **sp)
+        x2, r2 = kda.kda_residual_norm(y, r, nk["w_pre"], **p)
+        g2 = kda.kda_residual_norm_backward(y, r, nk["w_pre"], dx_out, None, **p)
+        gs = kda.kda_ssm_backward(u, ssm["dt"], ssm["B"], ssm["C"], ssm["A"], g2.dy.to(BF16), tiles, None, ssm["S0"], cu, **sp)
+        gc = kda.kda_short_conv_backward(x, conv["w"], gs.dx, cu, state_in=conv["state"], bias=conv["bias"])
+        g1 = kda.kda_residual_norm_backward(y0, nk["r"], nk["w_pre"], gc[0].to(BF16), g2.dr, **p)
+        return [x2, r2, S, *g1, *gc[:3], gs.dA]
+
+    out = block()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = block()
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = block()
+    g.replay()
+    torch.cuda.synchronize()
+    for a, b, c in zip(out, other, captured):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+    # against the oracle: each call's inputs are the last one's rounded outputs, so the chain is compared piece by piece
+    h = lambda v: None if v is None else host(v)
+    x_ref, r_ref = L.norm(h(y0), h(nk["r"]), h(nk["w_pre"]), h(nk["w_post"]), h(nk["gate"]), h(nk["scale"]), 0.75, 1e-5)
+    u_ref = L.conv(x_ref, h(conv["w"]), cu.cpu().numpy(), h(conv["state"]), h(conv["bias"]))[0]
+    y_ref, S_ref = L.ssm(u_ref, h(ssm["dt"]), h(ssm["B"]), h(ssm["C"]), h(ssm["A"]), h(ssm["S0"]), cu.cpu().numpy(), h(ssm["D"]),
+                         h(ssm["dt_bias"]), h(ssm["z"]))
+    x2_ref, r2_ref = L.norm(y_ref, r_ref, h(nk["w_pre"]), h(nk["w_post"]), h(nk["gate"]), h(nk["scale"]), 0.75, 1e-5)
+    # bf16 rounds x, u and y by 2^-8 each on the way (relative to rows of unit size): a few times that by norm
+    for got, ref in ((out[0], x2_ref), (out[1], r2_ref), (out[2], S_ref)):
+        assert np.linalg.norm(h(got) - ref) <= 4 * 2.0 ** -8 * np.linalg.norm(ref)
+
+
+def test_layer_other_device_is_refused_and_current_device_kept():
+    k = norm_case(2, 64, BF16, F32)
+    with pytest.raises(ValueError):
+        kda.kda_residual_norm(k["y"], k["r"].cpu(), k["w_pre"])
+    with pytest.raises(TypeError):
+        kda.kda_residual_norm(k["y"], k["r"], k["w_pre"].to(BF16))
+    with pytest.raises(ValueError):
+        kda.kda_residual_norm(k["y"].t(), None, None)
+    with pytest.raises(kda.KDAError):
+        kda.kda_residual_norm(randn(2, 12), None, randn(12))
+    assert torch.cuda.current_device() == 0
