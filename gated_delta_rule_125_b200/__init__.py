@@ -435,42 +435,37 @@ def kda_backward(q, k, v, log_alpha, beta, do, dS_T=None, S0=None, cu_seqlens=No
 # tensors of a device other than the current one, and take what they allocate from the pool of the
 # stream they run on.
 
-class _On:
-    """Makes the tensors' device current, and ``stream`` if one is given, for the duration of a call."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device, stream):
-        self._device, self._stream = device, stream
 
-    def __enter__(self):
-        self._was = torch.cuda.current_device()
-        if self._was != self._device.index:
-            torch.cuda.set_device(self._device)
-        if self._stream is not None:
-            self._before = torch.cuda.current_stream(self._device)
-            torch.cuda.set_stream(self._stream)
-        return ctypes.c_void_p(torch.cuda.current_stream(self._device).cuda_stream)
-
-    def __exit__(self, *exc):
-        if self._stream is not None:
-            torch.cuda.set_stream(self._before)
-        if self._was != self._device.index:
-            torch.cuda.set_device(self._was)
-        return False
+def _run(device, stream, body):
+    """``body(handle of the stream)`` with the tensors' device current, and ``stream`` if one is given."""
+    index = device.index
+    if stream is None:
+        if torch.cuda.current_device() == index:
+            return body(_raw_stream(index))
+        with torch.cuda.device(index):
+            return body(_raw_stream(index))
+    if stream.device != device:
+        raise ValueError("stream must be on %s, got %s" % (device, stream.device))
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
 
 def _arg(name, t, dtype, shape, device):
     """The address of a contiguous ``t`` of this dtype and shape on this device (None: NULL)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return t.data_ptr() or None
     if t.device != device:
         raise ValueError("%s must live on %s, got %s" % (name, device, t.device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr() or None
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _scratch(workspace, device):
@@ -524,25 +519,28 @@ def kda_ssm_prefill(x, dt, B, C, A, S0=None, cu_seqlens=None, *, D=None, dt_bias
     code = _dtype_code(x)
     N, pcu = _seqs(cu_seqlens, dev)
     f32, st = torch.float32, (N, p.channels, p.states)
-    with _On(dev, stream) as on:
+    def body(on):
+        nonlocal S_T, workspace, y
         if y is None:
             y = torch.empty_like(x)
         if S_T is None:
-            S_T = torch.empty(st, dtype=f32, device=dev)
+            S_T = A.new_empty(st) if S0 is None else torch.empty_like(S0)
         if workspace is None:
             nbytes = lib.kda_ssm_prefill_workspace_size(N, T, p.channels, p.states, p.groups)
             if nbytes:
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         tiles = None
         if save_states:
-            tiles = torch.empty((-(-T // KDA_SSM_TILE), p.channels, p.states), dtype=f32, device=dev)
+            tiles = A.new_empty((-(-T // KDA_SSM_TILE), p.channels, p.states))
         rc = lib.kda_ssm_prefill(px, pdt, pB, pC, pz, ctypes.byref(p), _arg("S0", S0, f32, st, dev), pcu, N, T, code,
                                  KDA_FLAG_SOFTPLUS if softplus else 0, _arg("y", y, x.dtype, x.shape, dev),
                                  _arg("S_T", S_T, f32, st, dev), _arg("tile states", tiles, f32, getattr(tiles, "shape", None), dev),
                                  *_scratch(workspace, dev), on)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_ssm_prefill")
-    return (y, S_T, tiles) if save_states else (y, S_T)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_ssm_prefill")
+        return (y, S_T, tiles) if save_states else (y, S_T)
+
+    return _run(dev, stream, body)
 
 
 def kda_ssm_step(x, dt, B, C, A, S, *, D=None, dt_bias=None, z=None, softplus=True, y=None, stream=None):
@@ -553,14 +551,17 @@ def kda_ssm_step(x, dt, B, C, A, S, *, D=None, dt_bias=None, z=None, softplus=Tr
     dev, N, p, (px, pdt, pB, pC, pz) = _ssm(x, dt, B, C, A, z, D, dt_bias)
     code = _dtype_code(x)
     pS = _arg("S", S, torch.float32, (N, p.channels, p.states), dev)
-    with _On(dev, stream) as on:
+    def body(on):
+        nonlocal y
         if y is None:
             y = torch.empty_like(x)
         rc = lib.kda_ssm_step(px, pdt, pB, pC, pz, ctypes.byref(p), pS, N, code, KDA_FLAG_SOFTPLUS if softplus else 0,
                               _arg("y", y, x.dtype, x.shape, dev), on)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_ssm_step")
-    return y
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_ssm_step")
+        return y
+
+    return _run(dev, stream, body)
 
 
 SsmGradients = collections.namedtuple("SsmGradients", "dx ddt dB dC dz dA dD ddt_bias dS0")
@@ -579,8 +580,9 @@ def kda_ssm_backward(x, dt, B, C, A, dy, tile_states, dS_T=None, S0=None, cu_seq
     f32, st = torch.float32, (N, p.channels, p.states)
     pt = _arg("tile_states", tile_states, f32, (-(-T // KDA_SSM_TILE), p.channels, p.states), dev)
     pdy, pdS, pS0 = _arg("dy", dy, x.dtype, x.shape, dev), _arg("dS_T", dS_T, f32, st, dev), _arg("S0", S0, f32, st, dev)
-    with _On(dev, stream) as on:
-        g = SsmGradients(*(None if t is None else torch.empty(t.shape, dtype=f32, device=dev)
+    def body(on):
+        nonlocal workspace
+        g = SsmGradients(*(None if t is None else torch.empty_like(t, dtype=f32)
                            for t in (x, dt, B, C, z, A, D, dt_bias, S0)))
         if workspace is None:
             nbytes = lib.kda_ssm_backward_workspace_size(N, T, p.channels, p.states, p.groups)
@@ -589,9 +591,11 @@ def kda_ssm_backward(x, dt, B, C, A, dy, tile_states, dS_T=None, S0=None, cu_seq
                                   KDA_FLAG_SOFTPLUS if softplus else 0, pt, pdy, pdS,
                                   ctypes.byref(SsmGrads(*(None if t is None else t.data_ptr() or None for t in g))),
                                   *_scratch(workspace, dev), on)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_ssm_backward")
-    return g
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_ssm_backward")
+        return g
+
+    return _run(dev, stream, body)
 
 
 def _conv_args(x, weight, bias, num_seqs, state_in, state_out):
@@ -610,13 +614,16 @@ def _conv_bias(x, weight, cu_seqlens, state_in, state_out, bias, y, stream):
     lib = load_library()
     N, pcu = _seqs(cu_seqlens, _cuda(x))
     dev, T, C, code, c, px, pb = _conv_args(x, weight, bias, N, state_in, state_out)
-    with _On(dev, stream) as on:
+    def body(on):
+        nonlocal y
         if y is None:
             y = torch.empty_like(x)
         rc = lib.kda_short_conv_swish_ex(px, _arg("y", y, x.dtype, x.shape, dev), ctypes.byref(c), pb, pcu, N, T, C, code, on)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_short_conv_swish")
-    return y
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_short_conv_swish")
+        return y
+
+    return _run(dev, stream, body)
 
 
 def kda_short_conv_step(x, weight, state, *, bias=None, y=None, stream=None):
@@ -625,13 +632,16 @@ def kda_short_conv_step(x, weight, state, *, bias=None, y=None, stream=None):
     dtype, shifted in place (None for W = 1). Returns y like x."""
     lib = load_library()
     dev, N, C, code, c, px, pb = _conv_args(x, weight, bias, x.shape[0], None, state)
-    with _On(dev, stream) as on:
+    def body(on):
+        nonlocal y
         if y is None:
             y = torch.empty_like(x)
         rc = lib.kda_short_conv_step(px, _arg("y", y, x.dtype, x.shape, dev), ctypes.byref(c), pb, N, C, code, on)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_short_conv_step")
-    return y
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_short_conv_step")
+        return y
+
+    return _run(dev, stream, body)
 
 
 def kda_short_conv_backward(x, weight, dy, cu_seqlens=None, *, bias=None, state_in=None, want_dstate=False,
@@ -644,9 +654,10 @@ def kda_short_conv_backward(x, weight, dy, cu_seqlens=None, *, bias=None, state_
     dev, T, C, code, c, px, pb = _conv_args(x, weight, bias, N, state_in, None)
     f32 = dict(dtype=torch.float32, device=dev)
     pdy = _arg("dy", dy, dy.dtype, x.shape, dev)
-    with _On(dev, stream) as on:
-        dx, dw = torch.empty(x.shape, **f32), torch.empty(weight.shape, **f32)
-        db = None if bias is None else torch.empty((C,), **f32)
+    def body(on):
+        nonlocal workspace
+        dx, dw = torch.empty_like(x, dtype=torch.float32), torch.empty_like(weight)
+        db = None if bias is None else torch.empty_like(bias)
         ds = torch.empty((N, weight.shape[1] - 1, C), **f32) if want_dstate else None
         if workspace is None:
             nbytes = lib.kda_short_conv_backward_workspace_size(T, C, weight.shape[1])
@@ -654,9 +665,11 @@ def kda_short_conv_backward(x, weight, dy, cu_seqlens=None, *, bias=None, state_
         rc = lib.kda_short_conv_backward(px, ctypes.byref(c), pb, pcu, N, T, C, code, pdy, _dtype_code(dy),
                                          dx.data_ptr() or None, dw.data_ptr(), None if db is None else db.data_ptr(),
                                          None if ds is None else ds.data_ptr() or None, *_scratch(workspace, dev), on)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_short_conv_backward")
-    return dx, dw, db, ds
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_short_conv_backward")
+        return dx, dw, db, ds
+
+    return _run(dev, stream, body)
 
 
 def _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps):
@@ -684,15 +697,18 @@ def kda_residual_norm(y, r=None, w_pre=None, *, w_post=None, gate=None, scale=No
     gate, scale 1). Returns ``(x, r_out)`` (x None without w_pre); ``r_out`` may be ``r``."""
     lib = load_library()
     dev, a, res = _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps)
-    with _On(dev, stream) as on:
+    def body(on):
+        nonlocal r_out, x
         if x is None and w_pre is not None:
             x = torch.empty_like(y)
         if r_out is None:
-            r_out = torch.empty(y.shape, dtype=res, device=dev)
+            r_out = torch.empty_like(y if r is None else r)
         rc = lib.kda_residual_norm(ctypes.byref(a), _arg("x", x, y.dtype, y.shape, dev), _arg("r_out", r_out, res, y.shape, dev), on)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_residual_norm")
-    return x, r_out
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_residual_norm")
+        return x, r_out
+
+    return _run(dev, stream, body)
 
 
 ResidualNormGradients = collections.namedtuple("ResidualNormGradients", "dy dr dgate dw_post dscale dw_pre")
@@ -706,14 +722,17 @@ def kda_residual_norm_backward(y, r, w_pre, dx, dr_out=None, *, w_post=None, gat
     lib = load_library()
     dev, a, _ = _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps)
     pdx, pdr = _arg("dx", dx, y.dtype, y.shape, dev), _arg("dr_out", dr_out, torch.float32, y.shape, dev)
-    with _On(dev, stream) as on:
-        g = ResidualNormGradients(*(None if t is None else torch.empty(t.shape, dtype=torch.float32, device=dev)
+    def body(on):
+        nonlocal workspace
+        g = ResidualNormGradients(*(None if t is None else torch.empty_like(t, dtype=torch.float32)
                                     for t in (y, r, gate, w_post, scale, w_pre)))
         if workspace is None:
             nbytes = lib.kda_residual_norm_backward_workspace_size(a.rows, a.D)
             workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
         rc = lib.kda_residual_norm_backward(ctypes.byref(a), pdx, pdr, *(None if t is None else t.data_ptr() or None for t in g),
                                             *_scratch(workspace, dev), on)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_residual_norm_backward")
-    return g
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_residual_norm_backward")
+        return g
+
+    return _run(dev, stream, body)

@@ -19,6 +19,18 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
+#ifndef CONV_SY
+#define CONV_SY 8
+#endif
+#ifndef CONV_BR
+#define CONV_BR 64
+#endif
+#ifndef CONV_R
+#define CONV_R 16
+#endif
+#ifndef CONV_A
+#define CONV_A 4
+#endif
 
 // The last s with cu[s] <= t: the sequence of token t (t < cu[N]; the empty ones before it are skipped).
 __device__ __forceinline__ int sequence_of(const int32_t *cu, int N, int64_t t) {
@@ -39,11 +51,21 @@ __device__ __forceinline__ void window_row(Pack8<T> &r, const T *x, const T *sta
     else r.zero();
 }
 
+// The taps of 8 channels lie together: 2 W loads of 16 bytes where w allows them.
 template <int W> __device__ __forceinline__ void load_taps(const float *w, int c0, float (&tap)[W][8]) {
+    const float *from = w + (size_t)c0 * W;
+    float v[8 * W];
+    if ((reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < 2 * W; ++i) *reinterpret_cast<float4 *>(v + 4 * i) = reinterpret_cast<const float4 *>(from)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8 * W; ++i) v[i] = from[i];
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < W; ++j) tap[j][i] = w[(size_t)(c0 + i) * W + j];
+        for (int j = 0; j < W; ++j) tap[j][i] = v[i * W + j];
 }
 
 __device__ __forceinline__ void load_bias(const float *bias, int c0, float (&v)[8]) {
@@ -53,8 +75,8 @@ __device__ __forceinline__ void load_bias(const float *bias, int c0, float (&v)[
 
 // ---- prompts ----
 
-constexpr int kRun = 16;                                        // tokens of a thread's run
-constexpr int ahead(int W) { return W > 4 ? 1 : 4; }            // rows loaded ahead (wide windows take the registers)
+constexpr int kRun = CONV_R;                                        // tokens of a thread's run
+constexpr int ahead(int W) { return W > 4 ? 1 : CONV_A; }            // rows loaded ahead (wide windows take the registers)
 
 template <int W, typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -181,7 +203,7 @@ conv_step_kernel(const ConvArgs a) {
 // and conv_sum_kernel adds the runs in order. A sequence's dstate is written by the thread of its first
 // token, which holds the g of its first W - 1 tokens.
 
-constexpr int kBackRun = 64;
+constexpr int kBackRun = CONV_BR;
 
 template <int W, typename T, typename TG>
 __global__ void __launch_bounds__(kThreads)
@@ -360,7 +382,7 @@ template <int W, typename T> cudaError_t launch_bias(const ConvArgs &a, cudaStre
 
 template <int W, typename T> cudaError_t launch_step(const ConvArgs &a, cudaStream_t st) {
     const unsigned gx = blocks(a.C / 8);
-    const unsigned gy = (unsigned)max(1, min(a.N, (int)((148 * 8 + gx - 1) / gx)));
+    const unsigned gy = (unsigned)max(1, min(a.N, (int)((148 * CONV_SY + gx - 1) / gx)));
     conv_step_kernel<W, T><<<dim3(gx, gy), kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
