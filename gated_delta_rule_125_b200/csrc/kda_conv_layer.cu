@@ -7,8 +7,9 @@
 //
 // rows before a sequence's first token being its initial state (which gets dx's share as dstate).
 //
-// All of it is bound by memory: x (and dy) read once, y (dx) written once. A thread owns 8 consecutive
-// channels (a 16-byte vector of bf16) of a run of consecutive tokens and keeps the window in registers.
+// All of it is bound by memory: x (and dy) read once, y (dx) written once. A thread owns 4 consecutive
+// channels of a run of consecutive tokens and keeps the window in registers (8 channels halve the loads and
+// double the registers: 117 us against 85 us for the backward of 8192 tokens x 4096 channels, W = 4).
 // It loads some rows ahead, so that enough bytes are in flight. The rows around its run that its
 // window needs are its neighbours' too and come from the L2 cache.
 #include <type_traits>
@@ -19,18 +20,6 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
-#ifndef CONV_SY
-#define CONV_SY 8
-#endif
-#ifndef CONV_BR
-#define CONV_BR 64
-#endif
-#ifndef CONV_R
-#define CONV_R 16
-#endif
-#ifndef CONV_A
-#define CONV_A 4
-#endif
 
 // The last s with cu[s] <= t: the sequence of token t (t < cu[N]; the empty ones before it are skipped).
 __device__ __forceinline__ int sequence_of(const int32_t *cu, int N, int64_t t) {
@@ -44,66 +33,66 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int N, int64_t t) 
 }
 
 // Row `pos` of a sequence that starts at token b (pos < 0: from its initial state, or zero).
-template <int W, typename T>
-__device__ __forceinline__ void window_row(Pack8<T> &r, const T *x, const T *state, int64_t b, int64_t pos, int s, int C) {
+template <int W, typename P, typename T>
+__device__ __forceinline__ void window_row(P &r, const T *x, const T *state, int64_t b, int64_t pos, int s, int C) {
     if (pos >= 0) r.load(x + (size_t)(b + pos) * C);
     else if (state) r.load(state + ((size_t)s * (W - 1) + (W - 1 + pos)) * C);
     else r.zero();
 }
 
-// The taps of 8 channels lie together: 2 W loads of 16 bytes where w allows them.
-template <int W> __device__ __forceinline__ void load_taps(const float *w, int c0, float (&tap)[W][8]) {
+// The taps of V channels lie together: loads of 16 bytes where w allows them.
+template <int W, int V> __device__ __forceinline__ void load_taps(const float *w, int c0, float (&tap)[W][V]) {
     const float *from = w + (size_t)c0 * W;
-    float v[8 * W];
+    float v[V * W];
     if ((reinterpret_cast<uintptr_t>(w) & 15) == 0) {
 #pragma unroll
-        for (int i = 0; i < 2 * W; ++i) *reinterpret_cast<float4 *>(v + 4 * i) = reinterpret_cast<const float4 *>(from)[i];
+        for (int i = 0; i < V * W / 4; ++i) *reinterpret_cast<float4 *>(v + 4 * i) = reinterpret_cast<const float4 *>(from)[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 8 * W; ++i) v[i] = from[i];
+        for (int i = 0; i < V * W; ++i) v[i] = from[i];
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int j = 0; j < W; ++j) tap[j][i] = v[i * W + j];
 }
 
-__device__ __forceinline__ void load_bias(const float *bias, int c0, float (&v)[8]) {
+template <int V> __device__ __forceinline__ void load_bias(const float *bias, int c0, float (&v)[V]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = bias ? bias[c0 + i] : 0.f;
+    for (int i = 0; i < V; ++i) v[i] = bias ? bias[c0 + i] : 0.f;
 }
 
 // ---- prompts ----
 
-constexpr int kRun = CONV_R;                                        // tokens of a thread's run
-constexpr int ahead(int W) { return W > 4 ? 1 : CONV_A; }            // rows loaded ahead (wide windows take the registers)
+constexpr int kRun = 16, kVec = 4;                         // tokens and channels of a thread's run
+constexpr int ahead(int W, int most) { return W > 4 ? 1 : most; }  // rows loaded ahead (wide windows take the registers)
 
-template <int W, typename T>
+template <int W, int V, typename T>
 __global__ void __launch_bounds__(kThreads)
 conv_bias_kernel(const ConvArgs a) {
-    constexpr int kAhead = ahead(W);
-    const int nv = a.C / 8;
+    constexpr int kAhead = ahead(W, 8);
+    const int nv = a.C / V;
     const int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x, t0 = g / nv * kRun;
-    const int c0 = (int)(g % nv) * 8;
+    const int c0 = (int)(g % nv) * V;
     const int64_t rows = a.cu ? a.cu[a.N] : a.total;
     if (t0 >= rows) return;
     const T *x = static_cast<const T *>(a.x) + c0;
     const T *st = a.state_in ? static_cast<const T *>(a.state_in) + c0 : nullptr;
     T *y = static_cast<T *>(a.y) + c0;
-    float tap[W][8], bias[8];
-    load_taps<W>(a.w, c0, tap);
+    float tap[W][V], bias[V];
+    load_taps<W, V>(a.w, c0, tap);
     load_bias(a.bias, c0, bias);
     int s = a.cu ? sequence_of(a.cu, a.N, t0) : 0;
     int64_t b = a.cu ? a.cu[s] : 0, e = a.cu ? a.cu[s + 1] : a.total;
     const int64_t t1 = min(t0 + kRun, rows);
-    Pack8<T> win[W];  // win[W - 1]: the current row
+    Pack<T, V> win[W];  // win[W - 1]: the current row
     auto fill = [&](int64_t t) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) window_row<W, T>(win[j], x, st, b, t - b - (W - 1) + j, s, a.C);
+        for (int j = 0; j < W - 1; ++j) window_row<W>(win[j], x, st, b, t - b - (W - 1) + j, s, a.C);
     };
     fill(t0);
     for (int64_t t = t0; t < t1; t += kAhead) {
-        Pack8<T> next[kAhead];
+        Pack<T, V> next[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) next[k].load(x + (size_t)min(t + k, t1 - 1) * a.C);
 #pragma unroll
@@ -118,18 +107,18 @@ conv_bias_kernel(const ConvArgs a) {
                 fill(t + k);
             }
             win[W - 1] = next[k];
-            float v[8], r[8];
+            float v[V], r[V];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = bias[i];
+            for (int i = 0; i < V; ++i) v[i] = bias[i];
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 win[j].get(r);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = fmaf(tap[j][i], r[i], v[i]);
+                for (int i = 0; i < V; ++i) v[i] = fmaf(tap[j][i], r[i], v[i]);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = silu_f(v[i]);
-            Pack8<T> o;
+            for (int i = 0; i < V; ++i) v[i] = silu_f(v[i]);
+            Pack<T, V> o;
             o.set(v);
             o.store_stream(y + (size_t)(t + k) * a.C);
 #pragma unroll
@@ -153,7 +142,7 @@ conv_last_kernel(const ConvArgs a) {
         T *to = static_cast<T *>(a.state_out) + c0;
         Pack8<T> r[W - 1];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) window_row<W, T>(r[j], x, st, b, e - b - (W - 1) + j, s, a.C);
+        for (int j = 0; j < W - 1; ++j) window_row<W>(r[j], x, st, b, e - b - (W - 1) + j, s, a.C);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) r[j].store(to + ((size_t)s * (W - 1) + j) * a.C);
     }
@@ -170,7 +159,7 @@ conv_step_kernel(const ConvArgs a) {
     const T *x = static_cast<const T *>(a.x) + c0;
     T *st = static_cast<T *>(a.state_out) + c0, *y = static_cast<T *>(a.y) + c0;
     float tap[W][8], bias[8];
-    load_taps<W>(a.w, c0, tap);
+    load_taps<W, 8>(a.w, c0, tap);
     load_bias(a.bias, c0, bias);
     for (int s = blockIdx.y; s < a.N; s += gridDim.y) {
         Pack8<T> win[W];
@@ -198,31 +187,33 @@ conv_step_kernel(const ConvArgs a) {
 
 // ---- gradients ----
 //
-// A thread's run of kBackRun tokens takes the g of its tokens and of the W - 1 behind them (which the
+// A thread's run takes the g of its tokens and of the W - 1 behind them (which the
 // next run forms too) and writes its dx. Its sums for dw and dbias go to the workspace, a row per run,
 // and conv_sum_kernel adds the runs in order. A sequence's dstate is written by the thread of its first
 // token, which holds the g of its first W - 1 tokens.
 
-constexpr int kBackRun = CONV_BR;
+// Long runs cost less (a row of partial sums each, W - 1 tokens formed twice), short ones fill the GPU:
+// 128 tokens where that leaves a thread for every lane of two CTAs per SM, else 32.
+int back_run(int64_t total, int C) { return total / 128 * (C / kVec) >= 148 * 2 * kThreads ? 128 : 32; }
 
-template <int W, typename T, typename TG>
+template <int W, int V, typename T, typename TG>
 __global__ void __launch_bounds__(kThreads)
-conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part) {
-    constexpr int kAhead = ahead(W);
+conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part, const int run_len) {
+    constexpr int kAhead = ahead(W, 4);
     const ConvArgs &a = p.f;
-    const int nv = a.C / 8;
-    const int64_t gid = (int64_t)blockIdx.x * kThreads + threadIdx.x, run = gid / nv, t0 = run * kBackRun;
+    const int nv = a.C / V;
+    const int64_t gid = (int64_t)blockIdx.x * kThreads + threadIdx.x, run = gid / nv, t0 = run * run_len;
     if (t0 >= a.total) return;
-    const int c0 = (int)(gid % nv) * 8;
+    const int c0 = (int)(gid % nv) * V;
     const int64_t rows = a.cu ? a.cu[a.N] : a.total;
     const T *x = static_cast<const T *>(a.x) + c0;
     const T *st = a.state_in ? static_cast<const T *>(a.state_in) + c0 : nullptr;
     const TG *dy = static_cast<const TG *>(p.dy) + c0;
-    float tap[W][8], bias[8], dw[W][8], db[8];
-    load_taps<W>(a.w, c0, tap);
+    float tap[W][V], bias[V], dw[W][V], db[V];
+    load_taps<W, V>(a.w, c0, tap);
     load_bias(a.bias, c0, bias);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < V; ++i) {
         db[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
@@ -230,19 +221,19 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part) {
     if (t0 < rows) {
         int s = a.cu ? sequence_of(a.cu, a.N, t0) : 0;
         int64_t b = a.cu ? a.cu[s] : 0, e = a.cu ? a.cu[s + 1] : a.total;
-        const int64_t t1 = min(t0 + kBackRun, rows), tl = min(t1 + W - 1, rows);  // the run, and what its dx needs
-        Pack8<T> win[W];
-        float acc[W][8];  // acc[j]: dx of row t - (W - 1) + j, so far
+        const int64_t t1 = min(t0 + run_len, rows), tl = min(t1 + W - 1, rows);  // the run, and what its dx needs
+        Pack<T, V> win[W];
+        float acc[W][V];  // acc[j]: dx of row t - (W - 1) + j, so far
         auto start = [&](int64_t t) {  // the window of token t of the current sequence, nothing summed yet
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) {
-                window_row<W, T>(win[j], x, st, b, t - b - (W - 1) + j, s, a.C);
+                window_row<W>(win[j], x, st, b, t - b - (W - 1) + j, s, a.C);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[j][i] = 0.f;
+                for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
             }
         };
         auto flush = [&](int64_t t, int j) {  // acc[j], of row t, is complete: dx, or a row of the initial state
-            Pack8<float> o;
+            Pack<float, V> o;
             o.set(acc[j]);
             if (t >= b) {
                 if (t >= t0 && t < t1) o.store_stream(p.dx + (size_t)t * a.C + c0);
@@ -252,8 +243,8 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part) {
         };
         start(t0);
         for (int64_t t = t0; t < tl; t += kAhead) {
-            Pack8<T> nx[kAhead];
-            Pack8<TG> ny[kAhead];
+            Pack<T, V> nx[kAhead];
+            Pack<TG, V> ny[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const size_t at = (size_t)min(t + k, tl - 1) * a.C;
@@ -280,9 +271,9 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part) {
                     start(tk);
                 }
                 win[W - 1] = nx[k];
-                float v[8], r[8], g[8];
+                float v[V], r[V], g[V];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < V; ++i) {
                     v[i] = bias[i];
                     acc[W - 1][i] = 0.f;
                 }
@@ -290,26 +281,26 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part) {
                 for (int j = 0; j < W; ++j) {
                     win[j].get(r);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = fmaf(tap[j][i], r[i], v[i]);
+                    for (int i = 0; i < V; ++i) v[i] = fmaf(tap[j][i], r[i], v[i]);
                 }
                 ny[k].get(g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < V; ++i) {
                     const float sg = sigmoid_f(v[i]);
                     g[i] *= sg * fmaf(v[i], 1.f - sg, 1.f);
                 }
 #pragma unroll
                 for (int j = 0; j < W; ++j)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[j][i] = fmaf(tap[j][i], g[i], acc[j][i]);
+                    for (int i = 0; i < V; ++i) acc[j][i] = fmaf(tap[j][i], g[i], acc[j][i]);
                 if (tk < t1) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) db[i] += g[i];
+                    for (int i = 0; i < V; ++i) db[i] += g[i];
 #pragma unroll
                     for (int j = 0; j < W; ++j) {
                         win[j].get(r);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dw[j][i] = fmaf(g[i], r[i], dw[j][i]);
+                        for (int i = 0; i < V; ++i) dw[j][i] = fmaf(g[i], r[i], dw[j][i]);
                     }
                 }
                 flush(tk - (W - 1), 0);
@@ -317,7 +308,7 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part) {
                 for (int j = 0; j < W - 1; ++j) {
                     win[j] = win[j + 1];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[j][i] = acc[j + 1][i];
+                    for (int i = 0; i < V; ++i) acc[j][i] = acc[j + 1][i];
                 }
             }
         }
@@ -330,7 +321,7 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part) {
     float *to = part + (size_t)run * (W + 1) * a.C + c0;
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
-        Pack8<float> o;
+        Pack<float, V> o;
         if (j < W) o.set(dw[j < W ? j : 0]);
         else o.set(db);
         o.store(to + (size_t)j * a.C);
@@ -374,7 +365,7 @@ unsigned blocks(int64_t n) { return (unsigned)((n + kThreads - 1) / kThreads); }
 
 template <int W, typename T> cudaError_t launch_bias(const ConvArgs &a, cudaStream_t st) {
     const int nv = a.C / 8;
-    if (a.total > 0) conv_bias_kernel<W, T><<<blocks((a.total + kRun - 1) / kRun * nv), kThreads, 0, st>>>(a);
+    if (a.total > 0) conv_bias_kernel<W, kVec, T><<<blocks((a.total + kRun - 1) / kRun * (a.C / kVec)), kThreads, 0, st>>>(a);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     if (W > 1 && a.state_out) conv_last_kernel<W, T><<<blocks((int64_t)a.N * nv), kThreads, 0, st>>>(a);
     return cudaGetLastError();
@@ -382,16 +373,17 @@ template <int W, typename T> cudaError_t launch_bias(const ConvArgs &a, cudaStre
 
 template <int W, typename T> cudaError_t launch_step(const ConvArgs &a, cudaStream_t st) {
     const unsigned gx = blocks(a.C / 8);
-    const unsigned gy = (unsigned)max(1, min(a.N, (int)((148 * CONV_SY + gx - 1) / gx)));
+    const unsigned gy = (unsigned)max(1, min(a.N, (int)((148 * 2 + gx - 1) / gx)));
     conv_step_kernel<W, T><<<dim3(gx, gy), kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
 template <int W, typename T, typename TG> cudaError_t launch_back(const ConvBackwardArgs &p, cudaStream_t st) {
     const ConvArgs &a = p.f;
-    const int64_t runs = (a.total + kBackRun - 1) / kBackRun;
+    const int run = back_run(a.total, a.C);
+    const int64_t runs = (a.total + run - 1) / run;
     float *part = static_cast<float *>(p.ws);
-    if (runs > 0) conv_backward_kernel<W, T, TG><<<blocks(runs * (a.C / 8)), kThreads, 0, st>>>(p, part);
+    if (runs > 0) conv_backward_kernel<W, kVec, T, TG><<<blocks(runs * (a.C / kVec)), kThreads, 0, st>>>(p, part, run);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     conv_sum_kernel<<<dim3((a.C + 31) / 32, W + 1), 256, 0, st>>>(part, runs, a.C, W, p.dw, p.dbias);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
@@ -429,7 +421,8 @@ cudaError_t conv_step(const ConvArgs &a, bool bf16, cudaStream_t st) {
 }
 
 size_t conv_backward_workspace(int64_t total, int C, int W) {
-    return (size_t)((total + kBackRun - 1) / kBackRun) * (W + 1) * C * sizeof(float);
+    const int run = back_run(total, C);
+    return (size_t)((total + run - 1) / run) * (W + 1) * C * sizeof(float);
 }
 
 cudaError_t conv_backward(const ConvBackwardArgs &p, bool bf16, cudaStream_t st) {

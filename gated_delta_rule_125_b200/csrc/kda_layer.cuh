@@ -69,6 +69,37 @@ template <> struct Pack8<float> {
     }
 };
 
+// Four consecutive channels likewise.
+template <typename T> struct Pack4;
+template <> struct Pack4<__nv_bfloat16> {
+    uint2 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
+    __device__ __forceinline__ void get(float (&x)[4]) const {
+        x[0] = __uint_as_float(u.x << 16), x[1] = __uint_as_float(u.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(u.y << 16), x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+    }
+    __device__ __forceinline__ void set(const float (&x)[4]) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+        u = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint2 *>(p) = u; }
+    __device__ __forceinline__ void store_stream(__nv_bfloat16 *p) const { __stcs(reinterpret_cast<uint2 *>(p), u); }
+};
+template <> struct Pack4<float> {
+    float4 a;
+    __device__ __forceinline__ void load(const float *p) { a = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void zero() { a = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w; }
+    __device__ __forceinline__ void set(const float (&x)[4]) { a = make_float4(x[0], x[1], x[2], x[3]); }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float4 *>(p) = a; }
+    __device__ __forceinline__ void store_stream(float *p) const { __stcs(reinterpret_cast<float4 *>(p), a); }
+};
+template <typename T, int V> struct PackOf;
+template <typename T> struct PackOf<T, 8> { using type = Pack8<T>; };
+template <typename T> struct PackOf<T, 4> { using type = Pack4<T>; };
+template <typename T, int V> using Pack = typename PackOf<T, V>::type;  // V channels
+
 // Copies 16 bytes to shared memory in the background (zeros where `on` is false).
 __device__ __forceinline__ void copy16(void *to, const void *from, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),

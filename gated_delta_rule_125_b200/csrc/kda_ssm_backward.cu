@@ -423,22 +423,35 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
     }
 }
 
-// dB, dC: the channel blocks' partial sums of each group, added in order.
+// dB, dC: the channel blocks' partial sums of each group, added by kSumLanes threads per value and then
+// over those, in order.
+constexpr int kSumLanes = 8;
 __global__ void __launch_bounds__(256)
 ssm_sum_kernel(const SsmArgs a, const int bpg, const float *__restrict__ pB, const float *__restrict__ pC,
                float *__restrict__ dB, float *__restrict__ dC) {
-    const int n4 = a.states / 4;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    __shared__ float4 red[kSumLanes][32];
+    const int n4 = a.states / 4, lane = threadIdx.x / 32, me = threadIdx.x % 32;
+    const int64_t i = (int64_t)blockIdx.x * 32 + me;
     const int64_t rows = a.cu ? a.cu[a.N] : a.total;
-    if (i >= rows * a.groups * n4) return;
-    const int64_t t = i / (a.groups * n4);
-    const int grp = (int)(i / n4 % a.groups), j = (int)(i % n4);
-    const float4 *from = reinterpret_cast<const float4 *>(blockIdx.y ? pC : pB) + ((size_t)grp * bpg * a.total + t) * n4 + j;
-    const size_t ld = (size_t)a.total * n4;
+    const bool on = i < rows * a.groups * n4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) {
+        const int64_t t = i / (a.groups * n4);
+        const int grp = (int)(i / n4 % a.groups), j = (int)(i % n4);
+        const float4 *from = reinterpret_cast<const float4 *>(blockIdx.y ? pC : pB) + ((size_t)grp * bpg * a.total + t) * n4 + j;
+        const size_t ld = (size_t)a.total * n4;
 #pragma unroll 8
-    for (int k = 0; k < bpg; ++k) {
-        const float4 w = __ldcs(from + k * ld);
+        for (int k = lane; k < bpg; k += kSumLanes) {
+            const float4 w = __ldcs(from + k * ld);
+            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+        }
+    }
+    red[lane][me] = v;
+    __syncthreads();
+    if (lane || !on) return;
+#pragma unroll
+    for (int k = 1; k < kSumLanes; ++k) {
+        const float4 w = red[k][me];
         v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
     }
     reinterpret_cast<float4 *>(blockIdx.y ? dC : dB)[i] = v;
@@ -487,7 +500,7 @@ cudaError_t launch_back(const SsmBackwardArgs &g, cudaStream_t st) {
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     if (a.total > 0) {
         const int64_t n = a.total * a.groups * (a.states / 4);
-        ssm_sum_kernel<<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, st>>>(a, bpg, pB, pC, g.dB, g.dC);
+        ssm_sum_kernel<<<dim3((unsigned)((n + 31) / 32), 2), 256, 0, st>>>(a, bpg, pB, pC, g.dB, g.dC);
         if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     }
     const int64_t n = (int64_t)a.channels * (a.states + 2);
