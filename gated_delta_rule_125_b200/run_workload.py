@@ -13,7 +13,10 @@ convolution fused into the loads), ``short_conv_8k`` (the convolution of one
 [8192, 32 * 128] projection), ``backward_1k`` (the backward of one 1024-token
 sequence, 32 heads), ``prefill_8k_conv`` (prefill_8k from raw projections with the
 width-4 short convolution of q, k, v inside the prefill), ``prefill_8k_gate`` (prefill_8k
-with the fused output step).
+with the fused output step); of the layer around the recurrences, each at 4096 channels in bf16:
+``ssm_prefill_2k`` and ``ssm_backward_1k`` (selective scan, 16 states, one sequence), ``ssm_step_256``
+(one token of 256 sequences), ``conv_backward_8k`` (short convolution with a bias, forward and
+backward), ``residual_norm_8k`` and ``residual_norm_backward_8k`` (the residual stream in fp32).
 """
 from __future__ import annotations
 
@@ -92,6 +95,31 @@ def main():
         for _ in range(args.calls):
             kda.kda_backward(inp["q"], inp["k"], inp["v"], inp["log_alpha"], inp["beta"], do, dST, inp["S0"],
                              inp["cu_seqlens"], max_seqlen=1024)
+    elif n in ("ssm_prefill_2k", "ssm_backward_1k", "ssm_step_256"):
+        T, N = {"ssm_prefill_2k": (2048, 1), "ssm_backward_1k": (1024, 1), "ssm_step_256": (256, 256)}[n]
+        i = KI.ssm_inputs(T, 4096, 16, 1, N, torch.bfloat16, dev)
+        x, dt, B, C, A, S0 = (i[k] for k in ("x", "dt", "B", "C", "A", "S0"))
+        kw = dict(D=i["D"], dt_bias=i["dt_bias"], z=i["z"])
+        for _ in range(args.calls):
+            if n == "ssm_step_256":
+                kda.kda_ssm_step(x, dt, B, C, A, S0, **kw)
+                continue
+            out = kda.kda_ssm_prefill(x, dt, B, C, A, S0, save_states=n != "ssm_prefill_2k", **kw)
+            if n == "ssm_backward_1k":
+                kda.kda_ssm_backward(x, dt, B, C, A, out[0], out[2], None, S0, **kw)
+    elif n == "conv_backward_8k":
+        x, w, st = KI.conv_inputs(8192, 4096, 4, 1, torch.bfloat16, dev)
+        bias = torch.zeros(4096, device=dev)
+        for _ in range(args.calls):
+            y = kda.kda_short_conv_swish(x, w, state_in=st, bias=bias)
+            kda.kda_short_conv_backward(x, w, y, state_in=st, bias=bias, want_dstate=True)
+    elif n in ("residual_norm_8k", "residual_norm_backward_8k"):
+        i = KI.norm_inputs(8192, 4096, torch.bfloat16, torch.float32, dev)
+        y, r, w_pre = i.pop("y"), i.pop("r"), i.pop("w_pre")
+        for _ in range(args.calls):
+            x, _ = kda.kda_residual_norm(y, r, w_pre, **i)
+            if "backward" in n:
+                kda.kda_residual_norm_backward(y, r, w_pre, x, r, **i)
     else:
         raise SystemExit("unknown workload %r" % n)
     torch.cuda.synchronize()

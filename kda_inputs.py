@@ -18,7 +18,13 @@ generator on the target device):
 * short-convolution inputs (the layer's q, k, v projections before the
   convolution): raw projections N(0, 1) in the workload dtype, taps
   N(0, 1/W) fp32 per channel, initial convolution states N(0, 1) in the
-  workload dtype.
+  workload dtype;
+* selective-scan inputs: x, B, C, z N(0, 1) and dt N(0, 0.5^2) in the workload
+  dtype, dt_bias such that softplus(dt_bias) is log-uniform in [0.001, 0.1],
+  A = -n exp(N(0, 0.1^2)) for state n = 1 .. states, D N(1, 0.1^2), initial
+  states N(0, 0.1^2) fp32;
+* residual-norm inputs: y, gate N(0, 1) in the workload dtype, r N(0, 2^2),
+  norm weights N(1, 0.1^2), scale N(0.5, 0.1^2) fp32.
 """
 from __future__ import annotations
 
@@ -28,7 +34,7 @@ import torch.nn.functional as F
 _BLOCK = 1 << 16  # tokens drawn per generator call (bounds fp32 temporaries)
 
 _IDS = {"q": 1, "k": 2, "v": 3, "beta": 4, "log_alpha": 5, "S0": 6, "len": 7, "log_alpha_scalar": 8,
-        "conv_x": 9, "conv_w": 10, "conv_state": 11}
+        "conv_x": 9, "conv_w": 10, "conv_state": 11, "ssm": 12, "norm": 13}
 
 
 def _gen(device, seed, name, block=0):
@@ -155,3 +161,22 @@ def conv_inputs(T, C, W, N=1, dtype=torch.bfloat16, device="cpu", seed=0, tensor
     if with_state:
         st = _normal((N, W - 1, C), device, seed * 3 + tensor, "conv_state").to(dtype)
     return x, w, st
+
+
+def ssm_inputs(T, channels, states, groups=1, N=1, dtype=torch.bfloat16, device="cpu", seed=0):
+    """Selective-scan inputs by the name of their argument: x, dt, z [T, channels], B, C [T, groups, states],
+    A [channels, states], D, dt_bias [channels], S0 [N, channels, states]."""
+    n = lambda i, *shape: _normal(shape, device, seed, "ssm", i)
+    step = torch.exp(torch.rand((channels,), generator=_gen(device, seed, "ssm", 9), device=device) * 4.605 - 6.908)
+    return dict(x=n(0, T, channels).to(dtype), dt=(0.5 * n(1, T, channels)).to(dtype), B=n(2, T, groups, states).to(dtype),
+                C=n(3, T, groups, states).to(dtype), z=n(4, T, channels).to(dtype),
+                A=-torch.arange(1, states + 1, device=device) * torch.exp(0.1 * n(5, channels, states)),
+                D=1 + 0.1 * n(6, channels), dt_bias=torch.log(torch.expm1(step)), S0=0.1 * n(7, N, channels, states))
+
+
+def norm_inputs(rows, D, dtype=torch.bfloat16, res_dtype=torch.float32, device="cpu", seed=0):
+    """Residual-norm inputs by the name of their argument: y, gate [rows, D], r [rows, D] in ``res_dtype``,
+    w_pre, w_post, scale [D]."""
+    n = lambda i, *shape: _normal(shape, device, seed, "norm", i)
+    return dict(y=n(0, rows, D).to(dtype), r=(2 * n(1, rows, D)).to(res_dtype), gate=n(2, rows, D).to(dtype),
+                w_pre=1 + 0.1 * n(3, D), w_post=1 + 0.1 * n(4, D), scale=0.5 + 0.1 * n(5, D))
