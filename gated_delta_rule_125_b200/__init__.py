@@ -435,6 +435,7 @@ def kda_backward(q, k, v, log_alpha, beta, do, dS_T=None, S0=None, cu_seqlens=No
 # tensors of a device other than the current one, and take what they allocate from the pool of the
 # stream they run on.
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -443,7 +444,7 @@ def _run(device, stream, body):
     """``body(handle of the stream)`` with the tensors' device current, and ``stream`` if one is given."""
     index = device.index
     if stream is None:
-        if torch.cuda.current_device() == index:
+        if _current_device() == index:
             return body(_raw_stream(index))
         with torch.cuda.device(index):
             return body(_raw_stream(index))
@@ -466,6 +467,14 @@ def _arg(name, t, dtype, shape, device):
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     raise ValueError("%s must be contiguous" % name)
+
+
+def _out(name, t, like, device):
+    """(``t``, its address): a caller's output checked against ``like``, or a new one."""
+    if t is None:
+        t = torch.empty_like(like)
+        return t, t.data_ptr() or None
+    return t, _arg(name, t, like.dtype, like.shape, device)
 
 
 def _scratch(workspace, device):
@@ -520,25 +529,19 @@ def kda_ssm_prefill(x, dt, B, C, A, S0=None, cu_seqlens=None, *, D=None, dt_bias
     N, pcu = _seqs(cu_seqlens, dev)
     f32, st = torch.float32, (N, p.channels, p.states)
     def body(on):
-        nonlocal S_T, workspace, y
-        if y is None:
-            y = torch.empty_like(x)
-        if S_T is None:
-            S_T = A.new_empty(st) if S0 is None else torch.empty_like(S0)
-        if workspace is None:
-            nbytes = lib.kda_ssm_prefill_workspace_size(N, T, p.channels, p.states, p.groups)
-            if nbytes:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        tiles = None
-        if save_states:
-            tiles = A.new_empty((-(-T // KDA_SSM_TILE), p.channels, p.states))
+        out, py = _out("y", y, x, dev)
+        last = S_T
+        if last is None:
+            last = A.new_empty(st) if S0 is None else torch.empty_like(S0)
+        nbytes = 0 if workspace is not None else lib.kda_ssm_prefill_workspace_size(N, T, p.channels, p.states, p.groups)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else workspace
+        tiles = A.new_empty((-(-T // KDA_SSM_TILE), p.channels, p.states)) if save_states else None
         rc = lib.kda_ssm_prefill(px, pdt, pB, pC, pz, ctypes.byref(p), _arg("S0", S0, f32, st, dev), pcu, N, T, code,
-                                 KDA_FLAG_SOFTPLUS if softplus else 0, _arg("y", y, x.dtype, x.shape, dev),
-                                 _arg("S_T", S_T, f32, st, dev), _arg("tile states", tiles, f32, getattr(tiles, "shape", None), dev),
-                                 *_scratch(workspace, dev), on)
+                                 KDA_FLAG_SOFTPLUS if softplus else 0, py, _arg("S_T", last, f32, st, dev),
+                                 tiles.data_ptr() or None if save_states else None, *_scratch(ws, dev), on)
         if rc != KDA_OK:
             raise KDAError(rc, "kda_ssm_prefill")
-        return (y, S_T, tiles) if save_states else (y, S_T)
+        return (out, last, tiles) if save_states else (out, last)
 
     return _run(dev, stream, body)
 
@@ -552,14 +555,12 @@ def kda_ssm_step(x, dt, B, C, A, S, *, D=None, dt_bias=None, z=None, softplus=Tr
     code = _dtype_code(x)
     pS = _arg("S", S, torch.float32, (N, p.channels, p.states), dev)
     def body(on):
-        nonlocal y
-        if y is None:
-            y = torch.empty_like(x)
+        out, py = _out("y", y, x, dev)
         rc = lib.kda_ssm_step(px, pdt, pB, pC, pz, ctypes.byref(p), pS, N, code, KDA_FLAG_SOFTPLUS if softplus else 0,
-                              _arg("y", y, x.dtype, x.shape, dev), on)
+                              py, on)
         if rc != KDA_OK:
             raise KDAError(rc, "kda_ssm_step")
-        return y
+        return out
 
     return _run(dev, stream, body)
 
@@ -615,13 +616,11 @@ def _conv_bias(x, weight, cu_seqlens, state_in, state_out, bias, y, stream):
     N, pcu = _seqs(cu_seqlens, _cuda(x))
     dev, T, C, code, c, px, pb = _conv_args(x, weight, bias, N, state_in, state_out)
     def body(on):
-        nonlocal y
-        if y is None:
-            y = torch.empty_like(x)
-        rc = lib.kda_short_conv_swish_ex(px, _arg("y", y, x.dtype, x.shape, dev), ctypes.byref(c), pb, pcu, N, T, C, code, on)
+        out, py = _out("y", y, x, dev)
+        rc = lib.kda_short_conv_swish_ex(px, py, ctypes.byref(c), pb, pcu, N, T, C, code, on)
         if rc != KDA_OK:
             raise KDAError(rc, "kda_short_conv_swish")
-        return y
+        return out
 
     return _run(dev, stream, body)
 
@@ -633,13 +632,11 @@ def kda_short_conv_step(x, weight, state, *, bias=None, y=None, stream=None):
     lib = load_library()
     dev, N, C, code, c, px, pb = _conv_args(x, weight, bias, x.shape[0], None, state)
     def body(on):
-        nonlocal y
-        if y is None:
-            y = torch.empty_like(x)
-        rc = lib.kda_short_conv_step(px, _arg("y", y, x.dtype, x.shape, dev), ctypes.byref(c), pb, N, C, code, on)
+        out, py = _out("y", y, x, dev)
+        rc = lib.kda_short_conv_step(px, py, ctypes.byref(c), pb, N, C, code, on)
         if rc != KDA_OK:
             raise KDAError(rc, "kda_short_conv_step")
-        return y
+        return out
 
     return _run(dev, stream, body)
 
@@ -673,7 +670,7 @@ def kda_short_conv_backward(x, weight, dy, cu_seqlens=None, *, bias=None, state_
 
 
 def _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps):
-    """Checks the norms' inputs; (device, kda_residual_norm_args, dtype of the residual stream)."""
+    """Checks the norms' inputs; (device, kda_residual_norm_args)."""
     dev = _cuda(y)
     D, rows = y.shape[-1], math.prod(y.shape[:-1])
     res = y.dtype if r is None else r.dtype
@@ -682,7 +679,7 @@ def _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps):
     return dev, ResidualNorm(_arg("y", y, y.dtype, y.shape, dev), _arg("r", r, res, y.shape, dev),
                              _arg("gate", gate, y.dtype, y.shape, dev), w("w_post", w_post), w("scale", scale),
                              w("w_pre", w_pre), float(res_scale), float(eps), rows, D, code,
-                             code if r is None else _dtype_code(r)), res
+                             code if r is None else _dtype_code(r))
 
 
 def kda_residual_norm(y, r=None, w_pre=None, *, w_post=None, gate=None, scale=None, res_scale=1.0, eps=1e-6, x=None,
@@ -696,17 +693,14 @@ def kda_residual_norm(y, r=None, w_pre=None, *, w_post=None, gate=None, scale=No
     Each of r, w_pre, w_post, gate, scale may be None (no stream yet, no norm before, no norm after, no
     gate, scale 1). Returns ``(x, r_out)`` (x None without w_pre); ``r_out`` may be ``r``."""
     lib = load_library()
-    dev, a, res = _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps)
+    dev, a = _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps)
     def body(on):
-        nonlocal r_out, x
-        if x is None and w_pre is not None:
-            x = torch.empty_like(y)
-        if r_out is None:
-            r_out = torch.empty_like(y if r is None else r)
-        rc = lib.kda_residual_norm(ctypes.byref(a), _arg("x", x, y.dtype, y.shape, dev), _arg("r_out", r_out, res, y.shape, dev), on)
+        new_x, px = (None, None) if x is None and w_pre is None else _out("x", x, y, dev)
+        new_r, pr = _out("r_out", r_out, y if r is None else r, dev)
+        rc = lib.kda_residual_norm(ctypes.byref(a), px, pr, on)
         if rc != KDA_OK:
             raise KDAError(rc, "kda_residual_norm")
-        return x, r_out
+        return new_x, new_r
 
     return _run(dev, stream, body)
 
@@ -720,7 +714,7 @@ def kda_residual_norm_backward(y, r, w_pre, dx, dr_out=None, *, w_post=None, gat
     ``dx = dL/dx`` (like y; None without w_pre) and ``dr_out = dL/dr_out`` (fp32, None: zero). Returns fp32
     ``ResidualNormGradients(dy, dr, dgate, dw_post, dscale, dw_pre)``, each None where its input is."""
     lib = load_library()
-    dev, a, _ = _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps)
+    dev, a = _norm_args(y, r, w_pre, w_post, gate, scale, res_scale, eps)
     pdx, pdr = _arg("dx", dx, y.dtype, y.shape, dev), _arg("dr_out", dr_out, torch.float32, y.shape, dev)
     def body(on):
         nonlocal workspace

@@ -11,21 +11,23 @@
 //
 // LPC lanes share a channel, NS states each, kept in registers as packed pairs (products and
 // multiply-adds two at a time), and walk the tokens of one sequence. Nothing but the chain of
-// multiply-adds waits for the token before: a batch's exponentials and products come first. The work
-// per (token, channel) -- softplus before, skip and gate after -- is done for a tile of 8 LPC tokens at
-// once, one token and 8 channels (a 16-byte vector of bf16) per thread; delta and delta x, and the sums
-// C h, pass through shared memory. Rows, B and C of the next tile are copied ahead by cp.async, each
-// thread to its own place; B and C are then expanded to fp32, read by all channels at one address.
+// multiply-adds waits for the token before: a batch's loads, products and exponentials are issued
+// before the steps of the batch in front of it. Sums over a channel's lanes are a reduce-scatter of
+// shuffles. Half of a CTA's warps do that; the other half do the work per (token, channel) for 32
+// tokens at a time, 8 channels (a 16-byte vector of bf16) per thread: softplus and the products before
+// the scan (tile i + 1 while the scan walks tile i), skip, gate and store after it (tile i - 1). They also
+// copy x, dt, z, B and C two tiles ahead (cp.async, each thread to its own place) and expand B and C to
+// fp32, read by all channels at one address.
 //
-// Where the channels alone do not fill the GPU the time axis is cut: one pass folds each segment from
-// a zero state into its end state and the sum of its steps (the decay of a whole segment is
-// e^(A sum delta), one exponential), ssm_join_kernel chains those, and the full pass starts each
-// segment from its true state. That takes the exponentials twice.
+// Where the channels leave most SMs idle the time axis is cut: one pass folds each segment from a zero
+// state into its end state and the sum of its steps (the decay of a whole segment is e^(A sum delta),
+// one exponential), ssm_join_kernel chains those, and the full pass starts each segment from its true
+// state. That takes the exponentials twice.
 //
-// Measured, 8192 tokens x 4096 channels x 16 states, bf16 with a gate: 418 us, 68 % of the rate of
-// exponentials that its two passes take. What it replaced: the time axis parallel inside a tile, lanes
-// combining (decay product, end state) pairs by a shuffle scan, every exponential once: 525 us (14
-// instructions per element and 41 % of the issue slots, too few warps to hide its chains).
+// Measured, 8192 tokens x 4096 channels x 16 states, bf16 with a gate: 381 us (0.70 TB/s; floors 41 us of
+// bytes, 145 us of exponentials: one warp of scan per SM quarter waits for its own chain). What it
+// replaced: the same without the split of the warps, time axis cut, 418 us; the time axis parallel inside a
+// tile, lanes combining (decay product, end state) pairs by a shuffle scan, 525 us.
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -99,49 +101,171 @@ __device__ __forceinline__ Segment segment_of(const int32_t *cu, int N, int64_t 
 
 enum { kFull, kSave, kFold };  // y and final states; tile states too; only the segments' ends
 
-// Shared memory of a CTA, and the sizes that follow from the lanes per channel.
+// Shared memory of a CTA, and the sizes that follow from the lanes per channel. Two tiles at a time: the
+// scan threads walk one while the others write the next and read the last one out.
+constexpr int TT = 32;  // tokens of a tile
 template <typename T, int NS, int LPC, int MODE> struct ScanMem {
     static constexpr int N_ = NS * LPC, CB = kScanThreads / LPC;  // states; channels of a CTA
-    static constexpr int TT = 8 * LPC;                  // tokens of a tile: one (token, 8 channels) piece per thread
     static constexpr int UT = LPC > 8 ? LPC : 8;        // tokens of a group
-    static constexpr int BT0 = 512 / N_ > UT ? 512 / N_ : UT, BT = BT0 < TT ? BT0 : TT;  // tokens of B and C staged at a time
-    static constexpr int PIECES = BT * N_ / 8, PK = (PIECES + kScanThreads - 1) / kScanThreads;
+    static constexpr int ROWS = TT * CB / 8, PR = (ROWS + kScanThreads - 1) / kScanThreads;      // pieces of 8 channels; per thread
+    static constexpr int PIECES = TT * N_ / 8, PK = (PIECES + kScanThreads - 1) / kScanThreads;  // pieces of 8 states of B (C); per thread
     static constexpr int kX = CB * 4 + 4, kY = CB + 4;  // words per token (padded: threads of consecutive tokens write)
-    static_assert(TT % BT == 0 && BT % UT == 0, "groups");
-    float sX[TT * kX];        // (delta, delta, delta x, delta x)
-    float sY[TT * kY];        // sum C h
-    float sBC[2][BT][2 * N_]; // (B, B, C, C) of two states
-    Pack8<T> sRow[2][MODE == kFold ? 2 : 3][kScanThreads];     // x, dt, z of the next tile: each thread's own piece
-    Pack8<T> sRaw[MODE == kFold ? 1 : 2][PK][kScanThreads];    // B and C likewise
+    float sX[2][TT * kX];     // (delta, delta, delta x, delta x)
+    float sY[2][TT * kY];     // sum C h
+    float sBC[2][TT][2 * N_]; // (B, B, C, C) of two states
+    Pack8<T> sRow[3][MODE == kFold ? 2 : 3][PR][kScanThreads];  // x, dt, z of three tiles: each thread's own pieces
+    Pack8<T> sRaw[MODE == kFold ? 1 : 2][PK][kScanThreads];     // B and C of the next tile likewise
 };
 
 template <typename T, int NS, int LPC, int MODE>
-__global__ void __launch_bounds__(kScanThreads, 4)
+__global__ void __launch_bounds__(2 * kScanThreads, 2)
 ssm_scan_kernel(const SsmArgs a, const int nblk, const int bpg, const int L, float *__restrict__ seg_state,
                 float *__restrict__ seg_step) {
     using M = ScanMem<T, NS, LPC, MODE>;
-    constexpr int N_ = M::N_, NP = NS / 2, CB = M::CB, TT = M::TT, UT = M::UT, BT = M::BT, PIECES = M::PIECES, PK = M::PK;
+    constexpr int N_ = M::N_, NP = NS / 2, CB = M::CB, UT = M::UT, PR = M::PR, PK = M::PK;
     constexpr int kX = M::kX, kY = M::kY, SU = NP < 8 ? 8 / NP : 1;  // tokens of a batch: 8 pairs of states
     extern __shared__ __align__(16) char smem_raw[];
     M &sm = *reinterpret_cast<M *>(smem_raw);
-    auto &sX = sm.sX;
-    auto &sY = sm.sY;
-    auto &sBC = sm.sBC;
-    auto &sRow = sm.sRow;
-    auto &sRaw = sm.sRaw;
-    const int tid = threadIdx.x, q = tid % LPC, ch = tid / LPC;
+    const int tid = threadIdx.x % kScanThreads;
     const int blk = blockIdx.x % nblk;
     const int64_t slot = blockIdx.x / nblk;
     const Segment g = segment_of(a.cu, a.N, a.total, slot, L);
     if (g.s < 0 || (MODE == kFold && g.last)) return;
     const int64_t b = g.t0;
-    const int len = g.len;
+    const int len = g.len, tiles = (len + TT - 1) / TT;
 
     const int cpg = a.channels / a.groups, grp = blk / bpg, c0 = (blk % bpg) * CB;
     const int nc = min(CB, cpg - c0);  // channels of this block (a multiple of 8)
-    const bool on = ch < nc;
     const int d0 = grp * cpg + c0;
-    const size_t ldx = a.channels, nstate = (size_t)a.channels * N_, own = (size_t)(d0 + (on ? ch : 0)) * N_ + q * NS;
+    const size_t ldx = a.channels, nstate = (size_t)a.channels * N_;
+
+    if (threadIdx.x >= kScanThreads) {
+        // ---- rows: copied ahead, made into steps and inputs before the scan, into outputs after it ----
+        const size_t ldb = (size_t)a.groups * N_;
+        const T *px = static_cast<const T *>(a.x) + b * ldx + d0, *pd = static_cast<const T *>(a.dt) + b * ldx + d0;
+        const T *pz = a.z ? static_cast<const T *>(a.z) + b * ldx + d0 : nullptr;
+        T *py = static_cast<T *>(a.y) + b * ldx + d0;
+        const T *Bp = static_cast<const T *>(a.B) + b * ldb + (size_t)grp * N_, *Cp = static_cast<const T *>(a.C) + b * ldb + (size_t)grp * N_;
+        float bias[PR][8], skip[PR][8];
+        bool mine[PR];
+#pragma unroll
+        for (int u = 0; u < PR; ++u) {
+            const int p = tid + u * kScanThreads, c = p / TT * 8;
+            mine[u] = p < M::ROWS && c < nc;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                bias[u][i] = mine[u] && a.dt_bias ? a.dt_bias[d0 + c + i] : 0.f;
+                skip[u][i] = mine[u] && a.D ? a.D[d0 + c + i] : 0.f;
+            }
+        }
+        auto copy_ahead = [&](int tile) {
+#pragma unroll
+            for (int u = 0; u < PR; ++u) {
+                const int p = tid + u * kScanThreads, t = tile * TT + p % TT;
+                const bool in = mine[u] && t < len;
+                const size_t at = in ? t * ldx + p / TT * 8 : 0;
+                copy8(&sm.sRow[tile % 3][0][u][tid], px + at, in);
+                copy8(&sm.sRow[tile % 3][1][u][tid], pd + at, in);
+                if constexpr (MODE != kFold) {
+                    if (pz) copy8(&sm.sRow[tile % 3][2][u][tid], pz + at, in);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < PK; ++u) {
+                const int p = tid + u * kScanThreads, t = tile * TT + p / (N_ / 8);
+                const bool in = p < M::PIECES && t < len;
+                const size_t at = in ? t * ldb + (p % (N_ / 8)) * 8 : 0;
+                copy8(&sm.sRaw[0][u][tid], Bp + at, in);
+                if constexpr (MODE != kFold) copy8(&sm.sRaw[1][u][tid], Cp + at, in);
+            }
+            copies_end_group();
+        };
+        auto before = [&](int tile) {
+            copies_wait<0>();
+            float *sX = sm.sX[tile & 1];
+#pragma unroll
+            for (int u = 0; u < PR; ++u) {
+                const int p = tid + u * kScanThreads, t = p % TT;
+                if (p >= M::ROWS) break;
+                float xv[8], dl[8];
+                sm.sRow[tile % 3][0][u][tid].get(xv);
+                sm.sRow[tile % 3][1][u][tid].get(dl);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dl[i] += bias[u][i];
+                if (a.softplus) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dl[i] = softplus_f(dl[i]);
+                }
+                const bool in = tile * TT + t < len;  // no step behind the last token
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float v = in ? dl[i] : 0.f, w = v * xv[i];
+                    *reinterpret_cast<float4 *>(sX + t * kX + (p / TT * 8 + i) * 4) = make_float4(v, v, w, w);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < PK; ++u) {
+                const int p = tid + u * kScanThreads;
+                if (p >= M::PIECES) break;
+                float v[8], w[8];
+                sm.sRaw[0][u][tid].get(v);
+                if constexpr (MODE != kFold) sm.sRaw[1][u][tid].get(w);
+                float4 *to = reinterpret_cast<float4 *>(sm.sBC[tile & 1][p / (N_ / 8)]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int pair = p % (N_ / 8) * 4 + i;  // pair pair % NP of lane pair / NP
+                    to[pair % NP * LPC + pair / NP] = make_float4(v[2 * i], v[2 * i + 1], w[2 * i], w[2 * i + 1]);
+                }
+            }
+        };
+        auto after = [&](int tile) {
+            if constexpr (MODE != kFold) {
+                const float *sY = sm.sY[tile & 1];
+#pragma unroll
+                for (int u = 0; u < PR; ++u) {
+                    const int p = tid + u * kScanThreads, t = p % TT, c = p / TT * 8;
+                    if (!mine[u] || tile * TT + t >= len) continue;
+                    float o[8], xv[8], zv[8];
+                    sm.sRow[tile % 3][0][u][tid].get(xv);
+                    sm.sRow[tile % 3][2][u][tid].get(zv);
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(sY + t * kY + c + i);
+                        o[i] = v.x, o[i + 1] = v.y, o[i + 2] = v.z, o[i + 3] = v.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        o[i] = fmaf(skip[u][i], xv[i], o[i]);
+                        if (pz) o[i] *= silu_f(zv[i]);
+                    }
+                    Pack8<T> w;
+                    w.set(o);
+                    w.store_stream(py + (size_t)(tile * TT + t) * ldx + c);
+                }
+            }
+        };
+        if (tiles) {
+            copy_ahead(0);
+            before(0);
+            if (tiles > 1) copy_ahead(1);
+        }
+        __syncthreads();
+        for (int i = 0; i < tiles; ++i) {
+            if (i) after(i - 1);
+            if (i + 1 < tiles) {
+                before(i + 1);
+                if (i + 2 < tiles) copy_ahead(i + 2);
+            }
+            __syncthreads();
+        }
+        if (tiles) after(tiles - 1);
+        return;
+    }
+
+    // ---- the scan ----
+    const int q = tid % LPC, ch = tid / LPC;
+    const bool on = ch < nc;
+    const size_t own = (size_t)(d0 + (on ? ch : 0)) * N_ + q * NS;
     F2 A[NP], h[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
@@ -157,147 +281,47 @@ ssm_scan_kernel(const SsmArgs a, const int nblk, const int bpg, const int L, flo
 #pragma unroll
         for (int p = 0; p < NP; ++p) *reinterpret_cast<unsigned long long *>(to + own + 2 * p) = h[p].v;
     };
-    if (len <= 0) {
-        if (a.S_T) put(a.S_T + g.s * nstate);
-        return;
-    }
-
-    // this thread's piece of a tile: token pt, channels pc .. pc + 7
-    const int pt = tid % TT, pc = tid / TT * 8;
-    const bool pon = pc < nc;
-    const size_t at0 = (b + pt) * ldx + d0 + pc;
-    float bias[8], skip[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = pon && a.dt_bias ? a.dt_bias[d0 + pc + i] : 0.f;
-        skip[i] = pon && a.D ? a.D[d0 + pc + i] : 0.f;
-    }
-    const T *px = static_cast<const T *>(a.x) + at0, *pd = static_cast<const T *>(a.dt) + at0;
-    const T *pz = a.z ? static_cast<const T *>(a.z) + at0 : nullptr;
-    T *py = static_cast<T *>(a.y) + at0;
-    auto load_rows = [&](int t0, int st) {
-        const bool in = pon && t0 + pt < len;
-        copy8(&sRow[st][0][tid], in ? px + t0 * ldx : px, in);
-        copy8(&sRow[st][1][tid], in ? pd + t0 * ldx : pd, in);
-        if constexpr (MODE != kFold) {
-            if (pz) copy8(&sRow[st][2][tid], in ? pz + t0 * ldx : pz, in);
-        }
-        copies_end_group();
-    };
-    const size_t ldb = (size_t)a.groups * N_;
-    const T *Bp = static_cast<const T *>(a.B) + b * ldb + (size_t)grp * N_, *Cp = static_cast<const T *>(a.C) + b * ldb + (size_t)grp * N_;
-    auto load_bc = [&](int t0) {
-#pragma unroll
-        for (int u = 0; u < PK; ++u) {
-            const int p = tid + u * kScanThreads, t = t0 + p / (N_ / 8);
-            const bool in = p < PIECES && t < len;
-            const size_t at = in ? t * ldb + (p % (N_ / 8)) * 8 : 0;
-            copy8(&sRaw[0][u][tid], Bp + at, in);
-            if constexpr (MODE != kFold) copy8(&sRaw[1][u][tid], Cp + at, in);
-        }
-        copies_end_group();
-    };
-    auto store_bc = [&](int buf) {
-#pragma unroll
-        for (int u = 0; u < PK; ++u) {
-            const int p = tid + u * kScanThreads;
-            if (p >= PIECES) continue;
-            float v[8], w[8];
-            sRaw[0][u][tid].get(v);
-            if constexpr (MODE != kFold) sRaw[1][u][tid].get(w);
-            float4 *to = reinterpret_cast<float4 *>(&sBC[buf][p / (N_ / 8)][0]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int pair = p % (N_ / 8) * 4 + i;  // pair pair % NP of lane pair / NP
-                to[pair % NP * LPC + pair / NP] = make_float4(v[2 * i], v[2 * i + 1], w[2 * i], w[2 * i + 1]);
-            }
-        }
-    };
-    load_rows(0, 0);
-    load_bc(0);
-    int buf = 0, st = 0;
     float sum = 0.f;  // of the steps (kFold)
-    for (int t0 = 0; t0 < len; t0 += TT, st ^= 1) {
-        // before: steps and inputs of the tile (no step behind the last token)
-        copies_wait<1>();  // the rows (the first B and C of the tile may be in flight)
-        {
-            float xv[8], dl[8];
-            sRow[st][0][tid].get(xv);
-            sRow[st][1][tid].get(dl);
-            const bool in = t0 + pt < len;
+    __syncthreads();
+    for (int tile = 0; tile < tiles; ++tile) {
+        const float *sX = sm.sX[tile & 1] + ch * 4;
+        float *sY = sm.sY[tile & 1];
+        // The next batch's loads, products and exponentials stand before the current one's steps: they fill the
+        // time that its chain of multiply-adds and its shuffles wait.
+        Batch<SU, NP, LPC> bt[2];
+        bt[0].load(A, sX, kX, &sm.sBC[tile & 1][0][q * 4], 2 * N_);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dl[i] += bias[i];
-            if (a.softplus) {
+        for (int tok = 0; tok < TT; tok += UT) {  // (behind the last token: no steps, nothing stored)
+            float out[UT];
+            const int mark = MODE == kSave ? (int)(-(b + tile * TT + tok)) & (kSsmTile - 1) : kSsmTile;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dl[i] = softplus_f(dl[i]);
-            }
+            for (int u0 = 0; u0 < UT; u0 += SU) {
+                const int k = (tok + u0) / SU, next = tok + u0 + SU;
+                if (next < TT) bt[(k + 1) & 1].load(A, sX + next * kX, kX, &sm.sBC[tile & 1][next][q * 4], 2 * N_);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float v = in ? dl[i] : 0.f, w = v * xv[i];
-                *reinterpret_cast<float4 *>(sX + pt * kX + (pc + i) * 4) = make_float4(v, v, w, w);
-            }
-        }
-        if (t0 + TT < len) load_rows(t0 + TT, st ^ 1);
-#pragma unroll 1
-        for (int v0 = 0; v0 < TT && t0 + v0 < len; v0 += BT, buf ^= 1) {
-            if (v0 == 0 && t0 + TT < len) copies_wait<1>();  // B and C (the next rows may be in flight)
-            else copies_wait<0>();
-            store_bc(buf);
-            __syncthreads();  // (the other buffer's readers have passed the barrier before)
-            if (t0 + v0 + BT < len) load_bc(t0 + v0 + BT);
-#pragma unroll 2
-            for (int v = 0; v < BT; v += UT) {  // (behind the last token: no steps, nothing stored)
-                const int tok = v0 + v;
-                const float *bc = &sBC[buf][v][q * 4];
-                float out[UT];
-                const int mark = MODE == kSave ? (int)(-(b + t0 + tok)) & (kSsmTile - 1) : kSsmTile;
-#pragma unroll
-                for (int u0 = 0; u0 < UT; u0 += SU) {
-                    Batch<SU, NP, LPC> bt;
-                    bt.load(A, sX + (tok + u0) * kX + ch * 4, kX, bc + u0 * 2 * N_, 2 * N_);
-#pragma unroll
-                    for (int i = 0; i < SU; ++i) {
-                        const int u = u0 + i;
-                        if (MODE == kSave && u == mark && t0 + tok + u < len) put(a.tiles + (b + t0 + tok + u) / kSsmTile * nstate);
-                        bt.template step<MODE != kFold>(h, i, out[u]);
-                        if (MODE == kFold) sum += sX[(tok + u) * kX + ch * 4];
-                    }
+                for (int i = 0; i < SU; ++i) {
+                    const int u = u0 + i;
+                    if (MODE == kSave && u == mark && tile * TT + tok + u < len)
+                        put(a.tiles + (b + tile * TT + tok + u) / kSsmTile * nstate);
+                    bt[k & 1].template step<MODE != kFold>(h, i, out[u]);
+                    if (MODE == kFold) sum += sX[(tok + u) * kX];
                 }
-                if (MODE == kFold) continue;
-                // sums over the channel's lanes: lane q keeps the tokens u = q mod LPC
-#pragma unroll
-                for (int m = LPC / 2; m > 0; m >>= 1) {
-#pragma unroll
-                    for (int u = 0; u < UT; ++u) {
-                        if (u & m || u % LPC >= 2 * m) continue;
-                        const float give = q & m ? out[u] : out[u + m], keep = q & m ? out[u + m] : out[u];
-                        out[u] = keep + __shfl_xor_sync(0xffffffffu, give, m);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < UT / LPC; ++k) sY[(tok + k * LPC + q) * kY + ch] = out[k * LPC];
             }
+            if (MODE == kFold) continue;
+            // sums over the channel's lanes: lane q keeps the tokens u = q mod LPC
+#pragma unroll
+            for (int m = LPC / 2; m > 0; m >>= 1) {
+#pragma unroll
+                for (int u = 0; u < UT; ++u) {
+                    if (u & m || u % LPC >= 2 * m) continue;
+                    const float give = q & m ? out[u] : out[u + m], keep = q & m ? out[u + m] : out[u];
+                    out[u] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < UT / LPC; ++k) sY[(tok + k * LPC + q) * kY + ch] = out[k * LPC];
         }
         __syncthreads();
-        // after: skip, gate, store
-        if (MODE != kFold && pon && t0 + pt < len) {
-            float o[8], xv[8], zv[8];
-            sRow[st][0][tid].get(xv);
-            if constexpr (MODE != kFold) sRow[st][2][tid].get(zv);
-#pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(sY + pt * kY + pc + i);
-                o[i] = v.x, o[i + 1] = v.y, o[i + 2] = v.z, o[i + 3] = v.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                o[i] = fmaf(skip[i], xv[i], o[i]);
-                if (pz) o[i] *= silu_f(zv[i]);
-            }
-            Pack8<T> w;
-            w.set(o);
-            w.store_stream(py + t0 * ldx);
-        }
     }
     if (MODE == kFold) {
         put(seg_state + slot * nstate);
@@ -345,43 +369,28 @@ ssm_join_kernel(const SsmArgs a, const int L, float *__restrict__ seg_state, con
 }
 
 // How the lanes and the time axis are dealt out.
-constexpr int kMinSegment = 256, kWantCtas = 148 * 8;
+constexpr int kMinSegment = 256;
+// Lanes of a channel. 16 states: four lanes 381 us for 8192 tokens of 4096 channels, eight 423 us (fewer
+// shuffles against more warps). 64 states: eight lanes 177 us for 6151 tokens of 1024 channels in 16
+// sequences, sixteen 221 us.
+constexpr int lanes_of(int states) { return states <= 16 ? 4 : 8; }
 struct Cut {
-    int lanes;  // lanes of a channel
-    int L;      // tokens of a segment
+    int L;  // tokens of a segment
     int nblk, bpg;
     int64_t slots;
     bool split;
 };
-int blocks_of(int channels, int groups, int lanes) {
-    const int CB = kScanThreads / lanes;
-    return (channels / groups + CB - 1) / CB * groups;
-}
-// 16 states: two lanes to a channel (the fewest shuffles and instructions) where that gives every SM
-// CTAs, else eight. 8192 tokens of 4096 channels: 418 us with two, 632 us with eight; 256 tokens of 128
-// channels: 37 us with two, 23 us with eight (of which about 20 are the host's). 64 states: sixteen
-// lanes 207 us, eight 216 us, four 269 us (6151 tokens of 1024 channels in 16 sequences).
-int lanes_of(int64_t total, int N, int channels, int states, int groups) {
-    switch (states) {
-    case 8: return 4;
-    case 16: return blocks_of(channels, groups, 2) * max((int64_t)N, total / kMinSegment) >= 2 * 148 ? 2 : 8;
-    case 64: return 16;
-    default: return 8;
-    }
-}
-// The time axis is cut when the sequences' channels give fewer CTAs than half of eight per SM (four at a
-// time are resident): 8192 tokens of 4096 channels 418 us against 490 us uncut (four lanes, its best).
+// The time axis is cut where the sequences' channels give a CTA to fewer than half of the SMs: a cut takes
+// the exponentials twice (8192 tokens of 4096 channels, 128 CTAs: 381 us uncut, 531 us in four segments).
 Cut cut_of(int64_t total, int N, int channels, int states, int groups) {
+    const int CB = kScanThreads / lanes_of(states);
     Cut c;
-    c.lanes = lanes_of(total, N, channels, states, groups);
-    c.nblk = blocks_of(channels, groups, c.lanes);
-    c.bpg = c.nblk / groups;
+    c.bpg = (channels / groups + CB - 1) / CB;
+    c.nblk = c.bpg * groups;
     int64_t L = total;
-    if ((int64_t)N * c.nblk * 2 <= kWantCtas) {
-        const int TT = 8 * c.lanes;  // whole tiles
-        const int64_t segs = kWantCtas / c.nblk;  // of all sequences
-        L = ((total + segs - 1) / segs + TT - 1) / TT * TT;
-        L = max(L, (int64_t)kMinSegment);
+    if ((int64_t)N * c.nblk * 2 <= 148) {
+        const int64_t segs = 148 / c.nblk;  // of all sequences
+        L = max(((total + segs - 1) / segs + TT - 1) / TT * TT, (int64_t)kMinSegment);
     }
     c.split = L < total;
     c.L = (int)max(min(L, total), (int64_t)1);
@@ -394,7 +403,7 @@ cudaError_t launch_mode(const SsmArgs &a, const Cut &c, unsigned grid, float *st
     auto kern = ssm_scan_kernel<T, NS, LPC, MODE>;
     constexpr int bytes = sizeof(ScanMem<T, NS, LPC, MODE>);
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); e != cudaSuccess) return e;
-    kern<<<grid, kScanThreads, bytes, st>>>(a, c.nblk, c.bpg, c.L, state, step);
+    kern<<<grid, 2 * kScanThreads, bytes, st>>>(a, c.nblk, c.bpg, c.L, state, step);
     return cudaGetLastError();
 }
 
@@ -416,9 +425,9 @@ cudaError_t prefill_t(const SsmArgs &a, void *ws, cudaStream_t st) {
     const Cut c = cut_of(a.total, a.N, a.channels, a.states, a.groups);
     switch (a.states) {
     case 8: return launch_scan<T, 2, 4>(a, c, ws, st);
-    case 16: return c.lanes == 2 ? launch_scan<T, 8, 2>(a, c, ws, st) : launch_scan<T, 2, 8>(a, c, ws, st);
+    case 16: return launch_scan<T, 4, 4>(a, c, ws, st);
     case 32: return launch_scan<T, 4, 8>(a, c, ws, st);
-    case 64: return launch_scan<T, 4, 16>(a, c, ws, st);
+    case 64: return launch_scan<T, 8, 8>(a, c, ws, st);
     case 128: return launch_scan<T, 16, 8>(a, c, ws, st);
     default: return cudaErrorInvalidValue;
     }

@@ -411,7 +411,7 @@ typedef struct kda_ssm {
  *
  *   workspace  kda_ssm_prefill_workspace_size() bytes of device scratch, 16-byte aligned (NULL where
  *              that is 0): 4 (states + 1) bytes per channel for each segment that long prompts are cut
- *              into when their channels alone do not fill the GPU.
+ *              into when their channels leave most of the GPU idle.
  *
  * Enqueued as kda_ssm_prefill_launches() kernels (1 to 3). Outputs must not overlap inputs (except
  * S_T == S0). Results do not depend on what the workspace held.

@@ -109,8 +109,8 @@ def test_ssm_null_structs(lib):
 def test_ssm_queries(lib):
     w, n = lib.kda_ssm_prefill_workspace_size, lib.kda_ssm_prefill_launches
     assert n(1, 128, 4096, 16, 1) == 1 and w(1, 128, 4096, 16, 1) == 0
-    assert n(1, 8192, 4096, 16, 1) == 3 and w(1, 8192, 4096, 16, 1) > 0
-    assert n(64, 8192, 8192, 16, 1) == 1 and w(64, 8192, 8192, 16, 1) == 0  # enough channels: uncut
+    assert n(1, 8192, 512, 16, 1) == 3 and w(1, 8192, 512, 16, 1) > 0
+    assert n(1, 8192, 4096, 16, 1) == 1 and w(1, 8192, 4096, 16, 1) == 0  # enough channels: uncut
     assert n(0, 128, 4096, 16, 1) == -1 and n(1, 128, 4096, 12, 1) == -1 and n(1, 128, 12, 16, 1) == -1
     b = lib.kda_ssm_backward_workspace_size
     assert 0 < b(1, 128, 64, 16, 1) < b(1, 256, 64, 16, 1) < b(1, 256, 128, 16, 1)

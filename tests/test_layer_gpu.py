@@ -244,7 +244,7 @@ def test_ssm_steps_continue_a_prompt():
 @pytest.mark.parametrize("lengths,ch,n,groups,dtype", [
     ([2100], 40, 16, 1, BF16),           # nine segments of 256 tokens, the last one short
     ([700, 0, 1300, 256, 3], 24, 8, 1, F32), ([513], 48, 32, 2, F32), ([1030, 600], 16, 64, 1, BF16), ([800], 8, 128, 1, F32),
-    ([2048, 1, 512], 1024, 16, 2, BF16),  # two lanes to a channel
+    ([2048, 1, 512], 256, 16, 2, BF16),
 ])
 def test_ssm_prefill_segments(lengths, ch, n, groups, dtype):
     """Long sequences cut into segments: outputs, final states and tile states."""
