@@ -146,7 +146,7 @@ def load_library():
     lib.kda_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.kda_set_wait_limit_ns.restype = ctypes.c_uint64
     sp = ctypes.POINTER(Ssm)
-    lib.kda_ssm_tile_states_size.argtypes = [i64, i32, i32]
+    lib.kda_ssm_tile_states_size.argtypes = [i32, i64, i32, i32]
     lib.kda_ssm_tile_states_size.restype = sz
     lib.kda_ssm_prefill_workspace_size.argtypes = lib.kda_ssm_prefill_launches.argtypes = [i32, i64, i32, i32, i32]
     lib.kda_ssm_prefill_workspace_size.restype, lib.kda_ssm_prefill_launches.restype = sz, i64
@@ -535,7 +535,7 @@ def kda_ssm_prefill(x, dt, B, C, A, S0=None, cu_seqlens=None, *, D=None, dt_bias
             last = A.new_empty(st) if S0 is None else torch.empty_like(S0)
         nbytes = 0 if workspace is not None else lib.kda_ssm_prefill_workspace_size(N, T, p.channels, p.states, p.groups)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else workspace
-        tiles = A.new_empty((-(-T // KDA_SSM_TILE), p.channels, p.states)) if save_states else None
+        tiles = A.new_empty((T // KDA_SSM_TILE + N, p.channels, p.states)) if save_states else None
         rc = lib.kda_ssm_prefill(px, pdt, pB, pC, pz, ctypes.byref(p), _arg("S0", S0, f32, st, dev), pcu, N, T, code,
                                  KDA_FLAG_SOFTPLUS if softplus else 0, py, _arg("S_T", last, f32, st, dev),
                                  tiles.data_ptr() or None if save_states else None, *_scratch(ws, dev), on)
@@ -579,7 +579,7 @@ def kda_ssm_backward(x, dt, B, C, A, dy, tile_states, dS_T=None, S0=None, cu_seq
     code = _dtype_code(x)
     N, pcu = _seqs(cu_seqlens, dev)
     f32, st = torch.float32, (N, p.channels, p.states)
-    pt = _arg("tile_states", tile_states, f32, (-(-T // KDA_SSM_TILE), p.channels, p.states), dev)
+    pt = _arg("tile_states", tile_states, f32, (T // KDA_SSM_TILE + N, p.channels, p.states), dev)
     pdy, pdS, pS0 = _arg("dy", dy, x.dtype, x.shape, dev), _arg("dS_T", dS_T, f32, st, dev), _arg("S0", S0, f32, st, dev)
     def body(on):
         nonlocal workspace

@@ -190,6 +190,10 @@ __device__ __forceinline__ F2 exp2_pair(F2 x) {
 
 constexpr int kSsmTile = 128;  // tokens of a tile (KDA_SSM_TILE)
 
+// First tile of sequence s, which starts at token b: its ceil(length / kSsmTile) tiles fit before the next
+// sequence's, and total / kSsmTile + N hold them all.
+__host__ __device__ __forceinline__ int64_t ssm_tile0(int64_t b, int s) { return b / kSsmTile + s; }
+
 struct SsmArgs {
     const void *x, *dt, *B, *C, *z;  // io dtype; z may be nullptr
     const float *A, *D, *dt_bias;    // [channels][states]; D, dt_bias [channels] or nullptr
@@ -201,7 +205,7 @@ struct SsmArgs {
     bool softplus;
     void *y;
     float *S_T;    // may be nullptr
-    float *tiles;  // [ceil(total / kSsmTile)][channels][states]: states before each tile, or nullptr
+    float *tiles;  // [total / kSsmTile + N][channels][states]: states before each tile (ssm_tile0), or nullptr
 };
 size_t ssm_prefill_workspace(int64_t total, int N, int channels, int states, int groups);
 int ssm_prefill_launches(int64_t total, int N, int channels, int states, int groups);

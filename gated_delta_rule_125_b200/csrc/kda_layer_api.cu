@@ -93,9 +93,9 @@ kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA
 
 extern "C" {
 
-size_t kda_ssm_tile_states_size(int64_t total_tokens, int32_t channels, int32_t states) {
-    if (total_tokens < 0 || channels < 1 || states < 1) return 0;
-    return (size_t)((total_tokens + kda::kSsmTile - 1) / kda::kSsmTile) * channels * states * sizeof(float);
+size_t kda_ssm_tile_states_size(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t states) {
+    if (num_seqs < 1 || total_tokens < 0 || channels < 1 || states < 1) return 0;
+    return (size_t)kda::ssm_tile0(total_tokens, num_seqs) * channels * states * sizeof(float);
 }
 
 size_t kda_ssm_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t states,

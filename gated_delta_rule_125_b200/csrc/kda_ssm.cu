@@ -286,6 +286,8 @@ ssm_scan_kernel(const SsmArgs a, const int nblk, const int bpg, const int L, flo
     for (int tile = 0; tile < tiles; ++tile) {
         const float *sX = sm.sX[tile & 1] + ch * 4;
         float *sY = sm.sY[tile & 1];
+        if (MODE == kSave && tile % (kSsmTile / TT) == 0)
+            put(a.tiles + (ssm_tile0(b - (int64_t)g.seg * L, g.s) + (g.seg * (int64_t)L + tile * TT) / kSsmTile) * nstate);
         // The next batch's loads, products and exponentials stand before the current one's steps: they fill the
         // time that its chain of multiply-adds and its shuffles wait.
         Batch<SU, NP, LPC> bt[2];
@@ -293,7 +295,6 @@ ssm_scan_kernel(const SsmArgs a, const int nblk, const int bpg, const int L, flo
 #pragma unroll
         for (int tok = 0; tok < TT; tok += UT) {  // (behind the last token: no steps, nothing stored)
             float out[UT];
-            const int mark = MODE == kSave ? (int)(-(b + tile * TT + tok)) & (kSsmTile - 1) : kSsmTile;
 #pragma unroll
             for (int u0 = 0; u0 < UT; u0 += SU) {
                 const int k = (tok + u0) / SU, next = tok + u0 + SU;
@@ -301,8 +302,6 @@ ssm_scan_kernel(const SsmArgs a, const int nblk, const int bpg, const int L, flo
 #pragma unroll
                 for (int i = 0; i < SU; ++i) {
                     const int u = u0 + i;
-                    if (MODE == kSave && u == mark && tile * TT + tok + u < len)
-                        put(a.tiles + (b + tile * TT + tok + u) / kSsmTile * nstate);
                     bt[k & 1].template step<MODE != kFold>(h, i, out[u]);
                     if (MODE == kFold) sum += sX[(tok + u) * kX];
                 }
@@ -390,7 +389,7 @@ Cut cut_of(int64_t total, int N, int channels, int states, int groups) {
     int64_t L = total;
     if ((int64_t)N * c.nblk * 2 <= 148) {
         const int64_t segs = 148 / c.nblk;  // of all sequences
-        L = max(((total + segs - 1) / segs + TT - 1) / TT * TT, (int64_t)kMinSegment);
+        L = max(((total + segs - 1) / segs + kSsmTile - 1) / kSsmTile * kSsmTile, (int64_t)kMinSegment);
     }
     c.split = L < total;
     c.L = (int)max(min(L, total), (int64_t)1);

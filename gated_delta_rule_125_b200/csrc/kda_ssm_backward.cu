@@ -109,10 +109,9 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
         dD[i] = db[i] = 0.f;
     }
 
-    const int64_t k0 = b / kSsmTile, k1 = e > b ? (e - 1) / kSsmTile : k0 - 1;
-    for (int64_t k = k1; k >= k0; --k) {
-        const int64_t t0 = max(b, k * kSsmTile);
-        const int len = (int)(min(e, (k + 1) * kSsmTile) - t0);
+    for (int64_t k = (e - b + kSsmTile - 1) / kSsmTile - 1; k >= 0; --k) {
+        const int64_t t0 = b + k * kSsmTile;
+        const int len = (int)min((int64_t)kSsmTile, e - t0);
         __syncthreads();  // the block before has been read out
 #pragma unroll 1
         for (int u = 0; u < PIECES; ++u) {
@@ -169,7 +168,7 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
 
         F2 h[NP];
         {
-            const float *from = t0 == b ? a.S0 ? a.S0 + s * nstate : nullptr : a.tiles + k * nstate;
+            const float *from = k == 0 ? a.S0 ? a.S0 + s * nstate : nullptr : a.tiles + (ssm_tile0(b, s) + k) * nstate;
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 h[p] = f2(0.f, 0.f);

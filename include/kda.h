@@ -404,11 +404,10 @@ typedef struct kda_ssm {
  *   S0, S_T    [N][channels][states] fp32 initial / final states: NULL = zeros / not written; S_T
  *              may alias S0. A sequence without tokens has S_T = S0.
  *   cu_seqlens as for kda_prefill. Rows from cu_seqlens[N] on are neither read nor written.
- *   tile_states  NULL, or [ceil(T / KDA_SSM_TILE)][channels][states] fp32, 16-byte aligned
- *              (kda_ssm_tile_states_size bytes): the state before each tile of KDA_SSM_TILE tokens
- *              of the packed axis, which kda_ssm_backward reads. Entries of tiles that start with
- *              the first token of a sequence are unspecified.
- *
+ *   tile_states  NULL, or kda_ssm_tile_states_size() bytes, 16-byte aligned: [T / KDA_SSM_TILE + N]
+ *              [channels][states] fp32, written with the state before each KDA_SSM_TILE tokens of every
+ *              sequence (sequence s from index cu_seqlens[s] / KDA_SSM_TILE + s on; entries between the
+ *              sequences are left as they were), for kda_ssm_backward.
  *   workspace  kda_ssm_prefill_workspace_size() bytes of device scratch, 16-byte aligned (NULL where
  *              that is 0): 4 (states + 1) bytes per channel for each segment that long prompts are cut
  *              into when their channels leave most of the GPU idle.
@@ -417,7 +416,7 @@ typedef struct kda_ssm {
  * S_T == S0). Results do not depend on what the workspace held.
  */
 #define KDA_SSM_TILE 128
-size_t kda_ssm_tile_states_size(int64_t total_tokens, int32_t channels, int32_t states);
+size_t kda_ssm_tile_states_size(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t states);
 size_t kda_ssm_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t states,
                                       int32_t groups);
 int64_t kda_ssm_prefill_launches(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t states,

@@ -66,8 +66,9 @@ def test_ssm_step_rejects(lib, over, code):
 
 def test_ssm_tile_states_size(lib):
     f = lib.kda_ssm_tile_states_size
-    assert f(0, 64, 16) == 0 and f(1, 64, 16) == f(128, 64, 16) == 64 * 16 * 4 and f(129, 64, 16) == 2 * f(1, 64, 16)
-    assert f(1 << 20, 8192, 128) == (1 << 13) * 8192 * 128 * 4 and f(-1, 64, 16) == 0 and f(5, 0, 16) == 0
+    assert f(1, 0, 64, 16) == f(1, 127, 64, 16) == 64 * 16 * 4 and f(1, 128, 64, 16) == 2 * 64 * 16 * 4 == f(2, 1, 64, 16)
+    assert f(1, 1 << 20, 8192, 128) == ((1 << 13) + 1) * 8192 * 128 * 4
+    assert f(0, 1, 64, 16) == 0 and f(1, -1, 64, 16) == 0 and f(1, 5, 0, 16) == 0
 
 
 def test_ssm_binding_checks():

@@ -199,17 +199,22 @@ def test_ssm_prefill_stream_and_graph():
         assert torch.equal(y3, y4) and torch.equal(S3, S4)
 
 
+def tile_states_check(k, tiles, lengths):
+    """The state before each 128 tokens of every sequence."""
+    h = ssm_host(k)
+    ref = L.ssm_states(**h)
+    mag = L.ssm_states(**{n: (np.abs(v) if n in ("x", "B", "S0") else v) for n, v in h.items()})
+    at = [(h["cu"][s] // 128 + s + j, h["cu"][s] + 128 * j) for s, m in enumerate(lengths) for j in range(-(-m // 128))]
+    assert len(set(i for i, _ in at)) == len(at) and max(i for i, _ in at) < tiles.shape[0] == sum(lengths) // 128 + len(lengths)
+    i, t = [list(v) for v in zip(*at)]
+    within(tiles[i], ref[t], mag[t], max(lengths) + 64, "tile states")
+
+
 def test_ssm_tile_states():
-    lengths = [300, 0, 84, 129]
+    lengths = [300, 0, 84, 129, 128, 1]
     k = ssm_case(lengths, 24, 16, dtype=F32, seed=13)
     _, _, tiles = ssm_run(k, save_states=True)
-    h = ssm_host(k)
-    ref = L.ssm_states(**h)[::128]
-    mag = L.ssm_states(**{n: (np.abs(v) if n in ("x", "B", "S0") else v) for n, v in h.items()})[::128]
-    starts = [i for i, t in enumerate(range(0, sum(lengths), 128)) if t in set(h["cu"][:-1])]
-    assert starts == [0, 3]  # token 384 is a sequence's first: its entry is unspecified
-    keep = [i for i in range(len(ref)) if i not in starts]
-    within(tiles[keep], ref[keep], mag[keep], 364)
+    tile_states_check(k, tiles, lengths)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -254,11 +259,7 @@ def test_ssm_prefill_segments(lengths, ch, n, groups, dtype):
     ws = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN where nothing is written
     y, S_T, tiles = ssm_run(k, save_states=True, workspace=ws)
     ssm_check(k, y, S_T, lengths)
-    h = ssm_host(k)
-    ref = L.ssm_states(**h)[::128]
-    mag = L.ssm_states(**{m: (np.abs(v) if m in ("x", "B", "S0") else v) for m, v in h.items()})[::128]
-    keep = [i for i, t in enumerate(range(0, sum(lengths), 128)) if t not in set(h["cu"][:-1])]
-    within(tiles[keep], ref[keep], mag[keep], max(lengths) + 64)
+    tile_states_check(k, tiles, lengths)
     again = ssm_run(k, workspace=ws)
     assert torch.equal(y, again[0]) and torch.equal(S_T, again[1])
 
