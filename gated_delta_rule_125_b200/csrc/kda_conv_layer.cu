@@ -39,6 +39,12 @@ __device__ __forceinline__ void window_row(P &r, const T *x, const T *state, int
     else if (state) r.load(state + ((size_t)s * (W - 1) + (W - 1 + pos)) * C);
     else r.zero();
 }
+template <int W, int V, typename T>
+__device__ __forceinline__ void window_row(float (&v)[V], const T *x, const T *state, int64_t b, int64_t pos, int s, int C) {
+    Pack<T, V> r;
+    window_row<W>(r, x, state, b, pos, s, C);
+    r.get(v);
+}
 
 // The taps of V channels lie together: loads of 16 bytes where w allows them.
 template <int W, int V> __device__ __forceinline__ void load_taps(const float *w, int c0, float (&tap)[W][V]) {
@@ -64,13 +70,13 @@ template <int V> __device__ __forceinline__ void load_bias(const float *bias, in
 
 // ---- prompts ----
 
-constexpr int kRun = 16, kVec = 4;                         // tokens and channels of a thread's run
-constexpr int ahead(int W, int most) { return W > 4 ? 1 : most; }  // rows loaded ahead (wide windows take the registers)
+constexpr int kRun = 32, kVec = 4;                         // tokens and channels of a thread's run
+constexpr int ahead(int W) { return W > 4 ? 1 : 4; }       // rows loaded together (wide windows take the registers)
 
 template <int W, int V, typename T>
 __global__ void __launch_bounds__(kThreads)
 conv_bias_kernel(const ConvArgs a) {
-    constexpr int kAhead = ahead(W, 8);
+    constexpr int kAhead = ahead(W);
     const int nv = a.C / V;
     const int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x, t0 = g / nv * kRun;
     const int c0 = (int)(g % nv) * V;
@@ -85,45 +91,57 @@ conv_bias_kernel(const ConvArgs a) {
     int s = a.cu ? sequence_of(a.cu, a.N, t0) : 0;
     int64_t b = a.cu ? a.cu[s] : 0, e = a.cu ? a.cu[s + 1] : a.total;
     const int64_t t1 = min(t0 + kRun, rows);
-    Pack<T, V> win[W];  // win[W - 1]: the current row
+    float win[W][V];  // win[W - 1]: the current row
     auto fill = [&](int64_t t) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) window_row<W>(win[j], x, st, b, t - b - (W - 1) + j, s, a.C);
+        for (int j = 0; j < W - 1; ++j) window_row<W, V>(win[j], x, st, b, t - b - (W - 1) + j, s, a.C);
     };
     fill(t0);
-    for (int64_t t = t0; t < t1; t += kAhead) {
+    // n tokens of the current sequence from t on (`whole`: kAhead of them)
+    auto tokens = [&](auto whole, int64_t t, int n) {
+        constexpr bool kWhole = decltype(whole)::value;
+        const T *px = x + (size_t)t * a.C;
+        T *py = y + (size_t)t * a.C;
         Pack<T, V> next[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) next[k].load(x + (size_t)min(t + k, t1 - 1) * a.C);
+        for (int k = 0; k < kAhead; ++k, px += a.C)
+            if (kWhole || k < n) next[k].load(px);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (t + k >= t1) break;
-            if (t + k == e) {
-                do {
-                    ++s;
-                    b = a.cu[s];
-                    e = a.cu[s + 1];
-                } while (e == b);
-                fill(t + k);
-            }
-            win[W - 1] = next[k];
-            float v[V], r[V];
+        for (int k = 0; k < kAhead; ++k, py += a.C) {
+            if (!kWhole && k >= n) break;
+            next[k].get(win[W - 1]);
+            float v[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = bias[i];
 #pragma unroll
             for (int j = 0; j < W; ++j) {
-                win[j].get(r);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = fmaf(tap[j][i], r[i], v[i]);
+                for (int i = 0; i < V; ++i) v[i] = fmaf(tap[j][i], win[j][i], v[i]);
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = silu_f(v[i]);
             Pack<T, V> o;
             o.set(v);
-            o.store_stream(y + (size_t)(t + k) * a.C);
+            o.store_stream(py);
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i];
         }
+    };
+    for (int64_t t = t0; t < t1;) {
+        if (t == e) {  // the next sequence (skipping the empty ones)
+            do {
+                ++s;
+                b = a.cu[s];
+                e = a.cu[s + 1];
+            } while (e == b);
+            fill(t);
+        }
+        const int n = (int)min((int64_t)kAhead, min(t1, e) - t);
+        if (n == kAhead) tokens(std::true_type{}, t, n);
+        else tokens(std::false_type{}, t, n);
+        t += n;
     }
 }
 
@@ -197,9 +215,9 @@ conv_step_kernel(const ConvArgs a) {
 int back_run(int64_t total, int C) { return total / 128 * (C / kVec) >= 148 * 2 * kThreads ? 128 : 32; }
 
 template <int W, int V, typename T, typename TG>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, W <= 4 ? 4 : 1)
 conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part, const int run_len) {
-    constexpr int kAhead = ahead(W, 4);
+    constexpr int kAhead = ahead(W);
     const ConvArgs &a = p.f;
     const int nv = a.C / V;
     const int64_t gid = (int64_t)blockIdx.x * kThreads + threadIdx.x, run = gid / nv, t0 = run * run_len;
@@ -222,12 +240,12 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part, const i
         int s = a.cu ? sequence_of(a.cu, a.N, t0) : 0;
         int64_t b = a.cu ? a.cu[s] : 0, e = a.cu ? a.cu[s + 1] : a.total;
         const int64_t t1 = min(t0 + run_len, rows), tl = min(t1 + W - 1, rows);  // the run, and what its dx needs
-        Pack<T, V> win[W];
+        float win[W][V];
         float acc[W][V];  // acc[j]: dx of row t - (W - 1) + j, so far
         auto start = [&](int64_t t) {  // the window of token t of the current sequence, nothing summed yet
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) {
-                window_row<W>(win[j], x, st, b, t - b - (W - 1) + j, s, a.C);
+                window_row<W, V>(win[j], x, st, b, t - b - (W - 1) + j, s, a.C);
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
             }
@@ -242,36 +260,26 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part, const i
             }
         };
         start(t0);
-        for (int64_t t = t0; t < tl; t += kAhead) {
+        // n tokens of the current sequence from t on (`inner`: kAhead of them, in the run, and so are the rows whose dx
+        // they complete)
+        auto tokens = [&](auto inner, int64_t t, int n) {
+            constexpr bool kInner = decltype(inner)::value;
+            const T *px = x + (size_t)t * a.C;
+            const TG *pg = dy + (size_t)t * a.C;
+            float *pd = p.dx + (size_t)(t - (W - 1)) * a.C + c0;
             Pack<T, V> nx[kAhead];
             Pack<TG, V> ny[kAhead];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const size_t at = (size_t)min(t + k, tl - 1) * a.C;
-                nx[k].load(x + at);
-                ny[k].load(dy + at);
+            for (int k = 0; k < kAhead; ++k, px += a.C, pg += a.C) {
+                if (!kInner && k >= n) break;
+                nx[k].load(px);
+                ny[k].load(pg);
             }
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int64_t tk = t + k;
-                if (tk >= tl) break;
-                if (tk == e) {  // the next sequence: what the last rows of this one have is all they get
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) flush(e - (W - 1) + j, j);
-                    if (tk >= t1) {
-                        t = tl;
-                        e = -1;
-                        break;
-                    }
-                    do {
-                        ++s;
-                        b = a.cu[s];
-                        e = a.cu[s + 1];
-                    } while (e == b);
-                    start(tk);
-                }
-                win[W - 1] = nx[k];
-                float v[V], r[V], g[V];
+            for (int k = 0; k < kAhead; ++k, pd += a.C) {
+                if (!kInner && k >= n) break;
+                nx[k].get(win[W - 1]);
+                float v[V], g[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     v[i] = bias[i];
@@ -279,9 +287,8 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part, const i
                 }
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
-                    win[j].get(r);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) v[i] = fmaf(tap[j][i], r[i], v[i]);
+                    for (int i = 0; i < V; ++i) v[i] = fmaf(tap[j][i], win[j][i], v[i]);
                 }
                 ny[k].get(g);
 #pragma unroll
@@ -293,24 +300,50 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part, const i
                 for (int j = 0; j < W; ++j)
 #pragma unroll
                     for (int i = 0; i < V; ++i) acc[j][i] = fmaf(tap[j][i], g[i], acc[j][i]);
-                if (tk < t1) {
+                if (kInner || t + k < t1) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) db[i] += g[i];
 #pragma unroll
                     for (int j = 0; j < W; ++j) {
-                        win[j].get(r);
 #pragma unroll
-                        for (int i = 0; i < V; ++i) dw[j][i] = fmaf(g[i], r[i], dw[j][i]);
+                        for (int i = 0; i < V; ++i) dw[j][i] = fmaf(g[i], win[j][i], dw[j][i]);
                     }
                 }
-                flush(tk - (W - 1), 0);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) {
-                    win[j] = win[j + 1];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) acc[j][i] = acc[j + 1][i];
+                if (kInner) {
+                    Pack<float, V> o;
+                    o.set(acc[0]);
+                    o.store_stream(pd);
+                } else {
+                    flush(t + k - (W - 1), 0);
                 }
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        win[j][i] = win[j + 1][i];
+                        acc[j][i] = acc[j + 1][i];
+                    }
             }
+        };
+        for (int64_t t = t0; t < tl;) {
+            if (t == e) {  // the next sequence: what the last rows of this one have is all they get
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) flush(e - (W - 1) + j, j);
+                if (t >= t1) {
+                    e = -1;
+                    break;
+                }
+                do {
+                    ++s;
+                    b = a.cu[s];
+                    e = a.cu[s + 1];
+                } while (e == b);
+                start(t);
+            }
+            const int n = (int)min((int64_t)kAhead, min(tl, e) - t);
+            if (n == kAhead && t - (W - 1) >= max(b, t0) && t + kAhead <= t1) tokens(std::true_type{}, t, n);
+            else tokens(std::false_type{}, t, n);
+            t += n;
         }
         if (e >= 0) {  // what is left: rows up to the last of the run (complete: their sequence, or the rows, end here)
 #pragma unroll
