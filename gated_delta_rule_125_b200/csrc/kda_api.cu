@@ -186,7 +186,7 @@ const char *kda_status_string(kda_status s) {
     return "KDA_ERR_UNKNOWN";
 }
 
-int32_t kda_version(void) { return 100; }
+int32_t kda_version(void) { return 200; }
 
 size_t kda_prefill_workspace_min(int32_t num_seqs, int64_t total_tokens, int32_t max_seqlen,
                                  int32_t H, int32_t dk, int32_t dv, kda_dtype dtype,

@@ -77,7 +77,8 @@ template <int SU, int NP, int LPC> struct Batch {
 // ceil(length / L) segments fit before the next sequence's; the rest stay empty).
 struct Segment {
     int s, seg, len;
-    int64_t t0;  // first token
+    int64_t t0;   // first token
+    int64_t end;  // slot of the sequence's last segment
     bool last;
 };
 __device__ __forceinline__ Segment segment_of(const int32_t *cu, int N, int64_t total, int64_t slot, int L) {
@@ -94,6 +95,7 @@ __device__ __forceinline__ Segment segment_of(const int32_t *cu, int N, int64_t 
     g.t0 = b + (int64_t)g.seg * L;
     const int64_t left = e - g.t0;
     g.len = (int)min((int64_t)L, left);
+    g.end = slot - g.seg + (e - b + L - 1) / L - 1;
     g.last = left <= L;
     if (left <= 0 && !(g.seg == 0 && left == 0)) g.s = -1;  // an empty slot
     return g;
@@ -272,8 +274,11 @@ ssm_scan_kernel(const SsmArgs a, const int nblk, const int bpg, const int L, flo
         const float2 v = *reinterpret_cast<const float2 *>(a.A + own + 2 * p);
         A[p] = f2(v.x * kLog2e, v.y * kLog2e);
         h[p] = f2(0.f, 0.f);
+        // A sequence in several segments: the last one may write S_T over S0 before the first one reads it, so the
+        // fold keeps S0 in the last segment's slot, which has no use for its own end state.
         const float *from = g.seg ? MODE == kFold ? nullptr : seg_state + (slot - 1) * nstate
-                                  : a.S0 ? a.S0 + g.s * nstate : nullptr;
+                            : !a.S0 ? nullptr
+                            : MODE == kFold || g.last ? a.S0 + g.s * nstate : seg_state + g.end * nstate;
         if (from) h[p].v = *reinterpret_cast<const unsigned long long *>(from + own + 2 * p);
     }
     auto put = [&](float *to) {
@@ -281,6 +286,7 @@ ssm_scan_kernel(const SsmArgs a, const int nblk, const int bpg, const int L, flo
 #pragma unroll
         for (int p = 0; p < NP; ++p) *reinterpret_cast<unsigned long long *>(to + own + 2 * p) = h[p].v;
     };
+    if (MODE == kFold && g.seg == 0) put(seg_state + g.end * nstate);
     float sum = 0.f;  // of the steps (kFold)
     __syncthreads();
     for (int tile = 0; tile < tiles; ++tile) {

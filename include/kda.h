@@ -429,7 +429,7 @@ kda_status kda_ssm_prefill(const void *x, const void *dt, const void *B, const v
 
 /*
  * One token of each of N sequences: x, dt, z, y [N][channels], B, C [N][groups][states] in dtype,
- * S [N][channels][states] fp32 updated in place. One launch.
+ * S [N][channels][states] fp32 updated in place. y must not overlap an input. One launch.
  */
 kda_status kda_ssm_step(const void *x, const void *dt, const void *B, const void *C, const void *z,
                         const kda_ssm *ssm, float *S, int32_t N, kda_dtype dtype, uint32_t flags, void *y,

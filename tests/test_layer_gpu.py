@@ -233,6 +233,39 @@ def test_ssm_step(N, ch, n, groups, dtype):
     ssm_check(k2, y, S, [1])
 
 
+def test_ssm_no_tokens():
+    """Only empty sequences: S_T = S0 (or zeros), gradients of the states pass through, the others are 0."""
+    k = ssm_case([0, 0, 0], 16, 8, dtype=BF16, seed=15)
+    y, S_T, tiles = ssm_run(k, save_states=True)
+    assert y.shape == (0, 16) and torch.equal(S_T, k["S0"])
+    assert (ssm_run(dict(k, S0=None))[1] == 0).all()
+    dS = randn(3, 16, 8, seed=16)
+    g = kda.kda_ssm_backward(k["x"], k["dt"], k["B"], k["C"], k["A"], k["x"], tiles, dS, k["S0"], k["cu"], D=k["D"],
+                             dt_bias=k["dt_bias"], z=k["z"])
+    assert torch.equal(g.dS0, dS) and all((v == 0).all() for v in (g.dA, g.dD, g.ddt_bias))
+    c = conv_case([0, 0], 16, 4, BF16, seed=17)
+    last = torch.empty_like(c["state"])
+    kda.kda_short_conv_swish(c["x"], c["w"], c["cu"], state_in=c["state"], state_out=last, bias=c["bias"])
+    assert torch.equal(last, c["state"])
+    d = kda.kda_short_conv_backward(c["x"], c["w"], c["x"].float(), c["cu"], bias=c["bias"], state_in=c["state"], want_dstate=True)
+    assert all((v == 0).all() for v in d[1:])
+
+
+def test_ssm_two_calls_at_once():
+    """Two prompts on two streams, each with its own workspace, and a third one behind them."""
+    a, b = ssm_case([3000], 64, 16, dtype=BF16, seed=18), ssm_case([2500, 700], 64, 16, dtype=BF16, seed=19)
+    assert kda.load_library().kda_ssm_prefill_launches(1, 3000, 64, 16, 1) > 1
+    ref = ssm_run(a), ssm_run(b)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = ssm_run(a, stream=streams[0]), ssm_run(b, stream=streams[1])
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        for u, v in zip(ref, got):
+            assert torch.equal(u[0], v[0]) and torch.equal(u[1], v[1])
+
+
 def test_ssm_steps_continue_a_prompt():
     k = ssm_case([60], 64, 16, dtype=F32, seed=14)
     y, S_T = ssm_run(k)
@@ -260,7 +293,9 @@ def test_ssm_prefill_segments(lengths, ch, n, groups, dtype):
     y, S_T, tiles = ssm_run(k, save_states=True, workspace=ws)
     ssm_check(k, y, S_T, lengths)
     tile_states_check(k, tiles, lengths)
-    again = ssm_run(k, workspace=ws)
+    # the final states over the initial ones, which the first segments read while the last ones write
+    S = k["S0"].clone()
+    again = ssm_run(dict(k, S0=S), S_T=S, workspace=ws)
     assert torch.equal(y, again[0]) and torch.equal(S_T, again[1])
 
 
