@@ -26,7 +26,7 @@ kda_status check_ssm_sizes(int32_t num_seqs, int64_t rows, int32_t channels, int
 kda_status check_ssm(const kda_ssm *p, int32_t num_seqs, int64_t rows, kda_dtype dtype, uint32_t flags) {
     if (!p || !known_dtype(dtype) || (flags & ~(uint32_t)KDA_FLAG_SOFTPLUS)) return KDA_ERR_INVALID_ARG;
     if (kda_status rc = check_ssm_sizes(num_seqs, rows, p->channels, p->states, p->groups); rc != KDA_OK) return rc;
-    if (rows > 0 && !p->A) return KDA_ERR_INVALID_ARG;
+    if (!p->A) return KDA_ERR_INVALID_ARG;
     if (!aligned16(p->A) || !aligned4(p->D, p->dt_bias)) return KDA_ERR_MISALIGNED;
     return KDA_OK;
 }
@@ -148,7 +148,7 @@ kda_status kda_ssm_backward(const void *x, const void *dt, const void *B, const 
                             const void *dy, const float *dS_T, const kda_ssm_grads *grads, void *workspace,
                             size_t workspace_bytes, kda_stream_t stream) {
     if (kda_status rc = check_ssm(ssm, num_seqs, total_tokens, dtype, flags); rc != KDA_OK) return rc;
-    if (!grads || !ssm->A || !grads->dA || (!cu_seqlens && num_seqs != 1)) return KDA_ERR_INVALID_ARG;
+    if (!grads || !grads->dA || (!cu_seqlens && num_seqs != 1)) return KDA_ERR_INVALID_ARG;
     const kda_ssm_grads &o = *grads;
     if (total_tokens > 0 && (!x || !dt || !B || !C || !dy || !tile_states || !o.dx || !o.ddt || !o.dB || !o.dC ||
                              (z != nullptr) != (o.dz != nullptr)))

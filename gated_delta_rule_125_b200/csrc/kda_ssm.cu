@@ -24,9 +24,9 @@
 // one exponential), ssm_join_kernel chains those, and the full pass starts each segment from its true
 // state. That takes the exponentials twice.
 //
-// Measured, 8192 tokens x 4096 channels x 16 states, bf16 with a gate: 381 us (0.70 TB/s; floors 41 us of
+// Measured, 8192 tokens x 4096 channels x 16 states, bf16 with a gate: 363 us (0.74 TB/s; floors 41 us of
 // bytes, 145 us of exponentials: one warp of scan per SM quarter waits for its own chain). What it
-// replaced: the same without the split of the warps, time axis cut, 418 us; the time axis parallel inside a
+// replaced: the same without the split of the warps, time axis cut, 409 us; the time axis parallel inside a
 // tile, lanes combining (decay product, end state) pairs by a shuffle scan, 525 us.
 #include "kda_layer.cuh"
 
@@ -461,7 +461,7 @@ cudaError_t ssm_prefill(const SsmArgs &a, void *ws, bool bf16, cudaStream_t st) 
 // sequences; a lane holds U 4-state vectors of them, n / 4 lanes to a channel, so every access is
 // a run of 16-byte vectors. The per-channel work (softplus, gate) is done by one lane per channel
 // and handed over by shuffles; C h is summed over a channel's lanes by shuffles. Measured, 256 sequences
-// x 4096 channels x 16 states in bf16 (148 MB): 31 us, 73 % of the copy rate.
+// x 4096 channels x 16 states in bf16 (143 MB): 31 us, 70 % of the copy rate.
 namespace {
 
 constexpr int kStepThreads = 128, kStepPerSm = 6;

@@ -51,7 +51,7 @@ def ssm_step(lib, **over):
 @no_gpu
 @pytest.mark.parametrize("over,code", SSM_BAD + [
     (dict(N=0), INVALID), (dict(N=3), INVALID), (dict(N=65536, cu=A), INVALID), (dict(T=-1), INVALID),
-    (dict(T=1 << 31), UNSUPPORTED), (dict(S0=A + 4), MISALIGNED), (dict(S_T=A + 8), MISALIGNED),
+    (dict(T=1 << 31), UNSUPPORTED), (dict(T=0, A=None), INVALID), (dict(S0=A + 4), MISALIGNED), (dict(S_T=A + 8), MISALIGNED),
     (dict(cu=A + 4, N=2), MISALIGNED), (dict(tiles=A + 4), MISALIGNED),
     (dict(ws=None), kda.KDA_ERR_WORKSPACE), (dict(wsb=64), kda.KDA_ERR_WORKSPACE), (dict(ws=A + 8), MISALIGNED)])
 def test_ssm_prefill_rejects(lib, over, code):
