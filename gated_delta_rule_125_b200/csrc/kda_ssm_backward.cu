@@ -141,6 +141,10 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
 #pragma unroll
                     for (int i = 0; i < 8; ++i) ev[i] *= silu_f(zv[i]);
                 }
+                // exp2_poly2's limits turn a NaN into a number: a step that is none goes into the chain here instead
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (dl[i] != dl[i]) ev[i] = dl[i];
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)

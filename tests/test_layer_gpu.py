@@ -413,6 +413,19 @@ def test_ssm_backward_same_bits_and_rows_behind():
         assert torch.equal(u, v[:240] if n in ("dx", "ddt", "dz", "dB", "dC") else v), n
 
 
+def test_ssm_backward_not_a_number_stays_in_sight():
+    """A NaN reaches the gradients that it reaches in the formulas, those of the tokens before it among them, and no
+    other sequence."""
+    k = ssm_case([200, 90], 24, 16, seed=31)
+    dy, dS = randn(290, 24, seed=32), randn(2, 24, 16, seed=33)
+    k["dt"][150, 5] = float("nan")
+    g = ssm_grad_run(k, dy, dS)
+    ref = L.ssm_backward(dy=host(dy), dS_T=host(dS), **ssm_host(k))
+    for name in g._fields:
+        np.testing.assert_array_equal(np.isnan(host(getattr(g, name))), np.isnan(ref[name]), err_msg=name)
+    assert np.isnan(ref["ddt"][:200, 5]).all() and np.isnan(ref["dB"][:151]).all() and not np.isnan(ref["dB"][200:]).any()
+
+
 def test_ssm_backward_differences():
     """The gradient of a step along a direction against the difference of two forward runs."""
     k, dy, dS = ssm_grad_case([90, 40], 16, 16, dtype=F32, seed=42)
