@@ -179,7 +179,7 @@ conv_step_kernel(const ConvArgs a) {
     float tap[W][8], bias[8];
     load_taps<W, 8>(a.w, c0, tap);
     load_bias(a.bias, c0, bias);
-    for (int s = blockIdx.y; s < a.N; s += gridDim.y) {
+    for (int64_t s = blockIdx.y; s < a.N; s += gridDim.y) {
         Pack8<T> win[W];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) win[j].load(st + ((size_t)s * (W - 1) + j) * a.C);

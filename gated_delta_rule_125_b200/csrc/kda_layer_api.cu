@@ -62,9 +62,9 @@ kda::ConvArgs conv_args(const void *x, void *y, const kda_short_conv *conv, cons
     return a;
 }
 
-bool overlap(const void *p, const void *q, size_t bytes) {
+bool overlap(const void *p, size_t np, const void *q, size_t nq) {  // p's np bytes and q's nq bytes
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + bytes && b < a + bytes;
+    return a < b + nq && b < a + np;
 }
 size_t size_of(kda_dtype t) { return t == KDA_DTYPE_BF16 ? 2 : 4; }
 
@@ -176,7 +176,8 @@ kda_status kda_short_conv_swish_ex(const void *x, void *y, const kda_short_conv 
     if (!cu_seqlens && num_seqs != 1) return KDA_ERR_INVALID_ARG;
     if (total_tokens > 0 && (!x || !y)) return KDA_ERR_INVALID_ARG;
     if (!aligned16(x, y, cu_seqlens)) return KDA_ERR_MISALIGNED;
-    if (total_tokens > 0 && overlap(x, y, (size_t)total_tokens * channels * size_of(dtype))) return KDA_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)total_tokens * channels * size_of(dtype);
+    if (total_tokens > 0 && overlap(x, bytes, y, bytes)) return KDA_ERR_INVALID_ARG;
     return done(kda::conv_bias(conv_args(x, y, conv, bias, cu_seqlens, num_seqs, total_tokens, channels),
                                dtype == KDA_DTYPE_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -187,7 +188,12 @@ kda_status kda_short_conv_step(const void *x, void *y, const kda_short_conv *con
     if (kda_status rc = check_conv(conv, bias, 1, N, channels, dtype); rc != KDA_OK) return rc;
     if (!x || !y || (conv->width > 1 && !conv->state_out)) return KDA_ERR_INVALID_ARG;
     if (!aligned16(x, y)) return KDA_ERR_MISALIGNED;
-    if (overlap(x, y, (size_t)N * channels * size_of(dtype))) return KDA_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)N * channels * size_of(dtype);
+    if (overlap(x, bytes, y, bytes)) return KDA_ERR_INVALID_ARG;
+    if (conv->width > 1) {  // the window is shifted while x is read and y is written
+        const size_t state = (conv->width - 1) * bytes;
+        if (overlap(x, bytes, conv->state_out, state) || overlap(y, bytes, conv->state_out, state)) return KDA_ERR_INVALID_ARG;
+    }
     return done(kda::conv_step(conv_args(x, y, conv, bias, nullptr, N, N, channels), dtype == KDA_DTYPE_BF16,
                                reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -209,6 +215,11 @@ kda_status kda_short_conv_backward(const void *x, const kda_short_conv *conv, co
     const size_t need = kda::conv_backward_workspace(total_tokens, channels, conv->width);
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if (!aligned16(x, dy, dx, dstate, workspace, cu_seqlens) || !aligned4(dweight, dbias)) return KDA_ERR_MISALIGNED;
+    if (total_tokens > 0) {  // a run of tokens reads the rows around it: dx in their place would change them
+        const size_t n = (size_t)total_tokens * channels;
+        if (overlap(dx, n * sizeof(float), x, n * size_of(dtype)) || overlap(dx, n * sizeof(float), dy, n * size_of(dy_dtype)))
+            return KDA_ERR_INVALID_ARG;
+    }
     kda::ConvBackwardArgs p{};
     p.f = conv_args(x, nullptr, conv, bias, cu_seqlens, num_seqs, total_tokens, channels);
     p.dy = dy; p.dy_bf16 = dy_dtype == KDA_DTYPE_BF16;

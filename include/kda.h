@@ -444,11 +444,11 @@ kda_status kda_ssm_step(const void *x, const void *dt, const void *B, const void
  *   dA [channels][states];   dD, ddt_bias [channels] or NULL (not written)
  *   dS0 [N][channels][states] or NULL (not written)
  *
- * All but dD and ddt_bias 16-byte aligned. Rows from cu_seqlens[N] on are neither read nor written.
- * Sums over channels, tokens and sequences are added in a fixed order (no atomics: the same bits every
- * call). workspace: kda_ssm_backward_workspace_size() bytes, 16-byte aligned (partial sums: 8 states
- * bytes per token for every 8 to 32 channels, and 4 (states + 2) per sequence and channel).
- * Three launches (two without tokens).
+ * All but dD and ddt_bias 16-byte aligned. No gradient may overlap an input or another gradient. Rows
+ * from cu_seqlens[N] on are neither read nor written. Sums over channels, tokens and sequences are added
+ * in a fixed order (no atomics: the same bits every call). workspace: kda_ssm_backward_workspace_size()
+ * bytes, 16-byte aligned (partial sums: 8 states bytes per token for every 8 to 32 channels, and
+ * 4 (states + 2) per sequence and channel). Three launches (two without tokens).
  */
 typedef struct kda_ssm_grads {
     float *dx;
@@ -482,7 +482,7 @@ kda_status kda_short_conv_swish_ex(const void *x, void *y, const kda_short_conv 
 /*
  * One token of each of N sequences: x, y [N][C], conv->state_out [N][W-1][C] read and shifted in place
  * (conv->state_in is not used; W = 1 needs no state). bias [C] fp32 or NULL. Windows 1 ..
- * KDA_MAX_CONV_WIDTH. y must not overlap x. One launch.
+ * KDA_MAX_CONV_WIDTH. x, y and the state must not overlap (KDA_ERR_INVALID_ARG). One launch.
  */
 kda_status kda_short_conv_step(const void *x, void *y, const kda_short_conv *conv, const float *bias, int32_t N,
                                int32_t channels, kda_dtype dtype, kda_stream_t stream);
@@ -496,8 +496,9 @@ kda_status kda_short_conv_step(const void *x, void *y, const kda_short_conv *con
  *   gradient of state_in) or NULL (not written). dx, dstate and workspace 16-byte aligned.
  *
  * Rows from cu_seqlens[N] on are neither read nor written. dweight and dbias are summed in a fixed
- * order (no atomics). workspace: kda_short_conv_backward_workspace_size() bytes (a partial dweight and
- * dbias per 64 tokens). Two launches, three with dstate and cu_seqlens.
+ * order (no atomics). dx must not overlap x or dy (KDA_ERR_INVALID_ARG), no output may overlap an input.
+ * workspace: kda_short_conv_backward_workspace_size() bytes (a partial dweight and dbias per 128 tokens,
+ * per 32 for calls that 128 would not fill the GPU with). Two launches, three with dstate and cu_seqlens.
  */
 size_t kda_short_conv_backward_workspace_size(int64_t total_tokens, int32_t channels, int32_t width);
 kda_status kda_short_conv_backward(const void *x, const kda_short_conv *conv, const float *bias,

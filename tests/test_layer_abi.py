@@ -158,6 +158,26 @@ def test_conv_backward_rejects(lib, over, code):
                                        a["dyt"], a["dx"], a["dw"], a["db"], a["ds"], a["ws"], a["wsb"], None) == code
 
 
+@no_gpu
+@pytest.mark.parametrize("over", [dict(), dict(x=A + 4096), dict(dy=A + 65536 - 16, x=A + (1 << 24)),
+                                  dict(dx=A + 32768 - 16, dy=A + (1 << 24)), dict(dyt=0, dx=A + 65536 - 16, x=A + (1 << 24))])
+def test_conv_backward_rejects_overlaps(lib, over):
+    """dx (65536 bytes here) in the place of x (32768) or dy (32768, fp32: 65536): the rows around a run are read from there."""
+    a = dict(x=A, dy=A, dyt=1, dx=A, w=A)
+    a.update(over)
+    c = ctypes.byref(kda.ShortConv(4, A, None, None))
+    assert lib.kda_short_conv_backward(a["x"], c, None, None, 1, 64, 256, 1, a["dy"], a["dyt"], a["dx"], A, None, None, A, 1 << 30,
+                                       None) == INVALID
+
+
+@no_gpu
+@pytest.mark.parametrize("x,y,state", [(A, A + 32768, A + 32768 - 16), (A, A + 32768, A + 65536 - 16), (A + 98304 - 16, A + (1 << 24), A)])
+def test_conv_step_rejects_overlaps(lib, x, y, state):
+    """x and y of 32768 bytes, the state of 98304."""
+    c = ctypes.byref(kda.ShortConv(4, A, None, state))
+    assert lib.kda_short_conv_step(x, y, c, None, 64, 256, 1, None) == INVALID
+
+
 NORM = dict(y=A, r=A, gate=A, w_post=A, scale=A, w_pre=A, res_scale=1.0, eps=1e-6, rows=4, D=64, dtype=1, res_dtype=0)
 NORM_BAD = [(dict(y=None), INVALID), (dict(rows=-1), INVALID), (dict(D=0), INVALID), (dict(D=12), INVALID), (dict(eps=0.0), INVALID),
             (dict(eps=float("nan")), INVALID), (dict(dtype=4), INVALID), (dict(res_dtype=4), INVALID), (dict(D=8200), UNSUPPORTED),
