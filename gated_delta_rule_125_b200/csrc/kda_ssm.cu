@@ -16,18 +16,21 @@
 // shuffles. Half of a CTA's warps do that; the other half do the work per (token, channel) for 32
 // tokens at a time, 8 channels (a 16-byte vector of bf16) per thread: softplus and the products before
 // the scan (tile i + 1 while the scan walks tile i), skip, gate and store after it (tile i - 1). They also
-// copy x, dt, z, B and C two tiles ahead (cp.async, each thread to its own place) and expand B and C to
-// fp32, read by all channels at one address.
+// copy x, dt, z, B and C two tiles ahead (cp.async, each thread to its own place) and lay B and C out for
+// the scan, whose loads from shared memory are what counts: a lane takes (delta, delta x) of two tokens in
+// one load, and B and C of bf16 inputs as they came (with both expanded to fp32 and each of delta, delta x
+// stored twice, ready for packed arithmetic, the loads kept shared memory 83 % busy: 363 us, not 323).
 //
 // Where the channels leave most SMs idle the time axis is cut: one pass folds each segment from a zero
 // state into its end state and the sum of its steps (the decay of a whole segment is e^(A sum delta),
 // one exponential), ssm_join_kernel chains those, and the full pass starts each segment from its true
 // state. That takes the exponentials twice.
 //
-// Measured, 8192 tokens x 4096 channels x 16 states, bf16 with a gate: 363 us (0.74 TB/s; floors 41 us of
-// bytes, 145 us of exponentials: one warp of scan per SM quarter waits for its own chain). What it
-// replaced: the same without the split of the warps, time axis cut, 409 us; the time axis parallel inside a
-// tile, lanes combining (decay product, end state) pairs by a shuffle scan, 525 us.
+// Measured, 8192 tokens x 4096 channels x 16 states, bf16 with a gate: 323 us (0.83 TB/s; floors 41 us of
+// bytes, 145 us of exponentials: one warp of scan per SM quarter waits for its own chain; with two CTAs to
+// an SM the exponentials are at 71 % of their rate). What it replaced, before those loads: no split of the
+// warps, time axis cut, 409 us; the time axis parallel inside a tile, lanes combining (decay product, end
+// state) pairs by a shuffle scan, 525 us.
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -35,22 +38,78 @@ namespace {
 
 constexpr int kScanThreads = 128;
 
+// B and C of a token in shared memory, by pairs of states: (B, C) of bf16 as they came, two pairs to 16
+// bytes, or (B, B, C, C) of fp32. Lane q of a channel owns the pairs q NP .. q NP + NP - 1.
+template <typename T, int NP, int LPC> struct Weights;
+template <int NP, int LPC> struct Weights<__nv_bfloat16, NP, LPC> {
+    static constexpr int kWords = 2 * NP * LPC;  // of a token
+    static __device__ __forceinline__ F2 wide(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+    // the states 8 j .. 8 j + 7
+    static __device__ __forceinline__ void put(float *row, int j, const Pack8<__nv_bfloat16> &b, const Pack8<__nv_bfloat16> &c) {
+        uint4 *to = reinterpret_cast<uint4 *>(row);
+        auto at = [](int pair) { return NP == 1 ? pair / 2 : pair % NP / 2 * LPC + pair / NP; };
+        to[at(4 * j)] = make_uint4(b.u.x, c.u.x, b.u.y, c.u.y);
+        to[at(4 * j + 2)] = make_uint4(b.u.z, c.u.z, b.u.w, c.u.w);
+    }
+    static __device__ __forceinline__ void get(const float *row, int q, F2 (&b)[NP], F2 (&c)[NP]) {
+        if constexpr (NP == 1) {
+            const uint2 w = reinterpret_cast<const uint2 *>(row)[q];
+            b[0] = wide(w.x), c[0] = wide(w.y);
+        } else {
+#pragma unroll
+            for (int v = 0; v < NP / 2; ++v) {
+                const uint4 w = reinterpret_cast<const uint4 *>(row)[v * LPC + q];
+                b[2 * v] = wide(w.x), c[2 * v] = wide(w.y);
+                b[2 * v + 1] = wide(w.z), c[2 * v + 1] = wide(w.w);
+            }
+        }
+    }
+};
+template <int NP, int LPC> struct Weights<float, NP, LPC> {
+    static constexpr int kWords = 4 * NP * LPC;
+    static __device__ __forceinline__ void put(float *row, int j, const Pack8<float> &b, const Pack8<float> &c) {
+        float v[8], w[8];
+        b.get(v);
+        c.get(w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int pair = 4 * j + i;
+            reinterpret_cast<float4 *>(row)[pair % NP * LPC + pair / NP] = make_float4(v[2 * i], v[2 * i + 1], w[2 * i], w[2 * i + 1]);
+        }
+    }
+    static __device__ __forceinline__ void get(const float *row, int q, F2 (&b)[NP], F2 (&c)[NP]) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const float4 g = reinterpret_cast<const float4 *>(row)[p * LPC + q];
+            b[p] = f2(g.x, g.y), c[p] = f2(g.z, g.w);
+        }
+    }
+};
+
 // What a batch of SU tokens needs that no state enters: decays, inputs, read-out weights of a lane's
-// states. w = (delta, delta, delta x, delta x) of a token, bc = (B, B, C, C) per pair of states.
-template <int SU, int NP, int LPC> struct Batch {
+// states. w = (delta, delta x) of a token and of the one behind it, bc the rows of B and C.
+template <typename T, int SU, int NP, int LPC> struct Batch {
     F2 e[SU][NP], in[SU][NP], c[SU][NP];
-    __device__ __forceinline__ void load(const F2 (&A)[NP], const float *w, int ldw, const float *bc, int ldbc) {
+    __device__ __forceinline__ void load(const F2 (&A)[NP], const float *sX, int ldw, const float *sBC, int t, int q) {
+        using W = Weights<T, NP, LPC>;
         F2 dl[SU];
+        float2 w[SU];
 #pragma unroll
         for (int u = 0; u < SU; ++u) {
-            const float4 v = *reinterpret_cast<const float4 *>(w + u * ldw);
-            dl[u] = f2(v.x, v.y);
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                const float4 g = *reinterpret_cast<const float4 *>(bc + u * ldbc + 4 * LPC * p);
-                in[u][p] = mul2(f2(v.z, v.w), f2(g.x, g.y));
-                c[u][p] = f2(g.z, g.w);
+            const float *from = sX + (t + u) / 2 * ldw;
+            if (SU % 2) {
+                w[u] = reinterpret_cast<const float2 *>(from)[(t + u) % 2];
+            } else if (u % 2 == 0) {
+                const float4 v = *reinterpret_cast<const float4 *>(from);
+                w[u] = make_float2(v.x, v.y), w[u + (SU > 1)] = make_float2(v.z, v.w);
             }
+        }
+#pragma unroll
+        for (int u = 0; u < SU; ++u) {
+            dl[u] = f2(w[u].x, w[u].x);
+            W::get(sBC + (t + u) * W::kWords, q, in[u], c[u]);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) in[u][p] = mul2(f2(w[u].y, w[u].y), in[u][p]);
         }
 #pragma unroll
         for (int u = 0; u < SU; ++u)
@@ -111,10 +170,11 @@ template <typename T, int NS, int LPC, int MODE> struct ScanMem {
     static constexpr int UT = LPC > 8 ? LPC : 8;        // tokens of a group
     static constexpr int ROWS = TT * CB / 8, PR = (ROWS + kScanThreads - 1) / kScanThreads;      // pieces of 8 channels; per thread
     static constexpr int PIECES = TT * N_ / 8, PK = (PIECES + kScanThreads - 1) / kScanThreads;  // pieces of 8 states of B (C); per thread
-    static constexpr int kX = CB * 4 + 4, kY = CB + 4;  // words per token (padded: threads of consecutive tokens write)
-    float sX[2][TT * kX];     // (delta, delta, delta x, delta x)
-    float sY[2][TT * kY];     // sum C h
-    float sBC[2][TT][2 * N_]; // (B, B, C, C) of two states
+    using W = Weights<T, NS / 2, LPC>;
+    static constexpr int kX = CB * 4 + 4, kY = CB + 4;  // words per two tokens, per token (padded: threads of consecutive tokens write)
+    float sX[2][TT / 2 * kX];     // (delta, delta x) of two tokens
+    float sY[2][TT * kY];         // sum C h
+    float sBC[2][TT * W::kWords]; // B and C
     Pack8<T> sRow[3][MODE == kFold ? 2 : 3][PR][kScanThreads];  // x, dt, z of three tiles: each thread's own pieces
     Pack8<T> sRaw[MODE == kFold ? 1 : 2][PK][kScanThreads];     // B and C of the next tile likewise
 };
@@ -202,22 +262,15 @@ ssm_scan_kernel(const SsmArgs a, const int nblk, const int bpg, const int L, flo
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float v = in ? dl[i] : 0.f, w = v * xv[i];
-                    *reinterpret_cast<float4 *>(sX + t * kX + (p / TT * 8 + i) * 4) = make_float4(v, v, w, w);
+                    *reinterpret_cast<float2 *>(sX + t / 2 * kX + (p / TT * 8 + i) * 4 + t % 2 * 2) = make_float2(v, w);
                 }
             }
 #pragma unroll
             for (int u = 0; u < PK; ++u) {
                 const int p = tid + u * kScanThreads;
                 if (p >= M::PIECES) break;
-                float v[8], w[8];
-                sm.sRaw[0][u][tid].get(v);
-                if constexpr (MODE != kFold) sm.sRaw[1][u][tid].get(w);
-                float4 *to = reinterpret_cast<float4 *>(sm.sBC[tile & 1][p / (N_ / 8)]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pair = p % (N_ / 8) * 4 + i;  // pair pair % NP of lane pair / NP
-                    to[pair % NP * LPC + pair / NP] = make_float4(v[2 * i], v[2 * i + 1], w[2 * i], w[2 * i + 1]);
-                }
+                M::W::put(sm.sBC[tile & 1] + p / (N_ / 8) * M::W::kWords, p % (N_ / 8), sm.sRaw[0][u][tid],
+                          sm.sRaw[MODE == kFold ? 0 : 1][u][tid]);  // (the fold has no use for C)
             }
         };
         auto after = [&](int tile) {
@@ -296,20 +349,20 @@ ssm_scan_kernel(const SsmArgs a, const int nblk, const int bpg, const int L, flo
             put(a.tiles + (ssm_tile0(b - (int64_t)g.seg * L, g.s) + (g.seg * (int64_t)L + tile * TT) / kSsmTile) * nstate);
         // The next batch's loads, products and exponentials stand before the current one's steps: they fill the
         // time that its chain of multiply-adds and its shuffles wait.
-        Batch<SU, NP, LPC> bt[2];
-        bt[0].load(A, sX, kX, &sm.sBC[tile & 1][0][q * 4], 2 * N_);
+        Batch<T, SU, NP, LPC> bt[2];
+        bt[0].load(A, sX, kX, sm.sBC[tile & 1], 0, q);
 #pragma unroll
         for (int tok = 0; tok < TT; tok += UT) {  // (behind the last token: no steps, nothing stored)
             float out[UT];
 #pragma unroll
             for (int u0 = 0; u0 < UT; u0 += SU) {
                 const int k = (tok + u0) / SU, next = tok + u0 + SU;
-                if (next < TT) bt[(k + 1) & 1].load(A, sX + next * kX, kX, &sm.sBC[tile & 1][next][q * 4], 2 * N_);
+                if (next < TT) bt[(k + 1) & 1].load(A, sX, kX, sm.sBC[tile & 1], next, q);
 #pragma unroll
                 for (int i = 0; i < SU; ++i) {
                     const int u = u0 + i;
                     bt[k & 1].template step<MODE != kFold>(h, i, out[u]);
-                    if (MODE == kFold) sum += sX[(tok + u) * kX];
+                    if (MODE == kFold) sum += sX[(tok + u) / 2 * kX + (tok + u) % 2 * 2];
                 }
             }
             if (MODE == kFold) continue;
