@@ -194,6 +194,54 @@ constexpr int kSsmTile = 128;  // tokens of a tile (KDA_SSM_TILE)
 // sequence's, and total / kSsmTile + N hold them all.
 __host__ __device__ __forceinline__ int64_t ssm_tile0(int64_t b, int s) { return b / kSsmTile + s; }
 
+// B and C of a token in shared memory, by pairs of states: (B, C) of bf16 as they came, two pairs to 16
+// bytes, or (B, B, C, C) of fp32. Lane q of a channel owns the pairs q NP .. q NP + NP - 1.
+template <typename T, int NP, int LPC> struct SsmWeights;
+template <int NP, int LPC> struct SsmWeights<__nv_bfloat16, NP, LPC> {
+    static constexpr int kWords = 2 * NP * LPC;  // of a token
+    static __device__ __forceinline__ F2 wide(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+    // the states 8 j .. 8 j + 7
+    static __device__ __forceinline__ void put(float *row, int j, const Pack8<__nv_bfloat16> &b, const Pack8<__nv_bfloat16> &c) {
+        uint4 *to = reinterpret_cast<uint4 *>(row);
+        auto at = [](int pair) { return NP == 1 ? pair / 2 : pair % NP / 2 * LPC + pair / NP; };
+        to[at(4 * j)] = make_uint4(b.u.x, c.u.x, b.u.y, c.u.y);
+        to[at(4 * j + 2)] = make_uint4(b.u.z, c.u.z, b.u.w, c.u.w);
+    }
+    static __device__ __forceinline__ void get(const float *row, int q, F2 (&b)[NP], F2 (&c)[NP]) {
+        if constexpr (NP == 1) {
+            const uint2 w = reinterpret_cast<const uint2 *>(row)[q];
+            b[0] = wide(w.x), c[0] = wide(w.y);
+        } else {
+#pragma unroll
+            for (int v = 0; v < NP / 2; ++v) {
+                const uint4 w = reinterpret_cast<const uint4 *>(row)[v * LPC + q];
+                b[2 * v] = wide(w.x), c[2 * v] = wide(w.y);
+                b[2 * v + 1] = wide(w.z), c[2 * v + 1] = wide(w.w);
+            }
+        }
+    }
+};
+template <int NP, int LPC> struct SsmWeights<float, NP, LPC> {
+    static constexpr int kWords = 4 * NP * LPC;
+    static __device__ __forceinline__ void put(float *row, int j, const Pack8<float> &b, const Pack8<float> &c) {
+        float v[8], w[8];
+        b.get(v);
+        c.get(w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int pair = 4 * j + i;
+            reinterpret_cast<float4 *>(row)[pair % NP * LPC + pair / NP] = make_float4(v[2 * i], v[2 * i + 1], w[2 * i], w[2 * i + 1]);
+        }
+    }
+    static __device__ __forceinline__ void get(const float *row, int q, F2 (&b)[NP], F2 (&c)[NP]) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const float4 g = reinterpret_cast<const float4 *>(row)[p * LPC + q];
+            b[p] = f2(g.x, g.y), c[p] = f2(g.z, g.w);
+        }
+    }
+};
+
 struct SsmArgs {
     const void *x, *dt, *B, *C, *z;  // io dtype; z may be nullptr
     const float *A, *D, *dt_bias;    // [channels][states]; D, dt_bias [channels] or nullptr

@@ -38,60 +38,12 @@ namespace {
 
 constexpr int kScanThreads = 128;
 
-// B and C of a token in shared memory, by pairs of states: (B, C) of bf16 as they came, two pairs to 16
-// bytes, or (B, B, C, C) of fp32. Lane q of a channel owns the pairs q NP .. q NP + NP - 1.
-template <typename T, int NP, int LPC> struct Weights;
-template <int NP, int LPC> struct Weights<__nv_bfloat16, NP, LPC> {
-    static constexpr int kWords = 2 * NP * LPC;  // of a token
-    static __device__ __forceinline__ F2 wide(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
-    // the states 8 j .. 8 j + 7
-    static __device__ __forceinline__ void put(float *row, int j, const Pack8<__nv_bfloat16> &b, const Pack8<__nv_bfloat16> &c) {
-        uint4 *to = reinterpret_cast<uint4 *>(row);
-        auto at = [](int pair) { return NP == 1 ? pair / 2 : pair % NP / 2 * LPC + pair / NP; };
-        to[at(4 * j)] = make_uint4(b.u.x, c.u.x, b.u.y, c.u.y);
-        to[at(4 * j + 2)] = make_uint4(b.u.z, c.u.z, b.u.w, c.u.w);
-    }
-    static __device__ __forceinline__ void get(const float *row, int q, F2 (&b)[NP], F2 (&c)[NP]) {
-        if constexpr (NP == 1) {
-            const uint2 w = reinterpret_cast<const uint2 *>(row)[q];
-            b[0] = wide(w.x), c[0] = wide(w.y);
-        } else {
-#pragma unroll
-            for (int v = 0; v < NP / 2; ++v) {
-                const uint4 w = reinterpret_cast<const uint4 *>(row)[v * LPC + q];
-                b[2 * v] = wide(w.x), c[2 * v] = wide(w.y);
-                b[2 * v + 1] = wide(w.z), c[2 * v + 1] = wide(w.w);
-            }
-        }
-    }
-};
-template <int NP, int LPC> struct Weights<float, NP, LPC> {
-    static constexpr int kWords = 4 * NP * LPC;
-    static __device__ __forceinline__ void put(float *row, int j, const Pack8<float> &b, const Pack8<float> &c) {
-        float v[8], w[8];
-        b.get(v);
-        c.get(w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int pair = 4 * j + i;
-            reinterpret_cast<float4 *>(row)[pair % NP * LPC + pair / NP] = make_float4(v[2 * i], v[2 * i + 1], w[2 * i], w[2 * i + 1]);
-        }
-    }
-    static __device__ __forceinline__ void get(const float *row, int q, F2 (&b)[NP], F2 (&c)[NP]) {
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const float4 g = reinterpret_cast<const float4 *>(row)[p * LPC + q];
-            b[p] = f2(g.x, g.y), c[p] = f2(g.z, g.w);
-        }
-    }
-};
-
 // What a batch of SU tokens needs that no state enters: decays, inputs, read-out weights of a lane's
 // states. w = (delta, delta x) of a token and of the one behind it, bc the rows of B and C.
 template <typename T, int SU, int NP, int LPC> struct Batch {
     F2 e[SU][NP], in[SU][NP], c[SU][NP];
     __device__ __forceinline__ void load(const F2 (&A)[NP], const float *sX, int ldw, const float *sBC, int t, int q) {
-        using W = Weights<T, NP, LPC>;
+        using W = SsmWeights<T, NP, LPC>;
         F2 dl[SU];
         float2 w[SU];
 #pragma unroll
@@ -170,7 +122,7 @@ template <typename T, int NS, int LPC, int MODE> struct ScanMem {
     static constexpr int UT = LPC > 8 ? LPC : 8;        // tokens of a group
     static constexpr int ROWS = TT * CB / 8, PR = (ROWS + kScanThreads - 1) / kScanThreads;      // pieces of 8 channels; per thread
     static constexpr int PIECES = TT * N_ / 8, PK = (PIECES + kScanThreads - 1) / kScanThreads;  // pieces of 8 states of B (C); per thread
-    using W = Weights<T, NS / 2, LPC>;
+    using W = SsmWeights<T, NS / 2, LPC>;
     static constexpr int kX = CB * 4 + 4, kY = CB + 4;  // words per two tokens, per token (padded: threads of consecutive tokens write)
     float sX[2][TT / 2 * kX];     // (delta, delta x) of two tokens
     float sY[2][TT * kY];         // sum C h

@@ -13,13 +13,22 @@
 // walks its tokens backwards in blocks of 128, from the state before each block that the forward
 // saved. It first folds the block forwards, keeping the state before each group of UG tokens; then,
 // group by group from the end, it forms the group's decays and states again in registers and runs the
-// reverse recurrence over them. So each exponential is taken twice and no state goes to memory.
+// reverse recurrence over them. So each exponential is taken twice and no state goes to memory. A block's
+// rows (x, dt, dy, z) are loaded together, the next block's on their way to the L2 cache meanwhile; B and C
+// are loaded a stage of up to 32 tokens ahead.
 // (h_t - delta x B in place of a h_(t-1) would save a product, and its relative accuracy.)
 //
 // Sums over the states (three per token and channel) are a reduce-scatter of shuffles over a
 // channel's lanes. Sums over the channels (dB, dC) are one over the lanes of the same states, then the
 // CTA's warps through shared memory, then its partial sums go to the workspace and ssm_sum_kernel adds
 // them in a fixed order: no atomics, the same bits every time.
+//
+// Measured, 4096 tokens (the longest sequence 2853) x 4096 channels x 16 states, bf16 with a gate: 694 us
+// with 24 more for the sums over the channels. Two warps per SM quarter (224 registers) issue in 52 % of the
+// clocks; the shared memory's pipe is 56 % busy, half of that with shuffles. What it replaced: every load
+// waited for where it is used 735 us, with B and C expanded to fp32 in shared memory; three CTAs to an SM
+// (registers capped without spills) 790 us, as the longest sequence's chain then gets a third of an SM (8
+// sequences of 512 tokens, which balance: 734 us with two CTAs, 703 us with three).
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -51,25 +60,32 @@ __device__ __forceinline__ F2 exp2_poly2(F2 x) {
               __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23)));
 }
 
-template <int NS, int LPC> struct BackMem {
+template <typename T, int NS, int LPC> struct BackMem {
     static constexpr int N_ = NS * LPC, CB = kThreads / LPC;
     static constexpr int UG = 16 / NS;                       // tokens of a group: 16 (token, state) values per lane
     static constexpr int BT = 512 / N_ > 32 ? 32 : 512 / N_; // tokens of B and C staged at a time
     static constexpr int EB = NS >= 8 ? 32 : kSsmTile;       // tokens whose groups' states fit shared memory
     static constexpr int kX = CB * 4 + 4;
     static_assert(EB % BT == 0 && BT % UG == 0 && kSsmTile % BT == 0, "groups");
+    // Where token v of the staged ones has its sums: two warps' parts of 16 states in a row of banks belong to the tokens
+    // v and v + 2 (written) or v and v + 1 (read).
+    static __host__ __device__ constexpr int slot(int v) { return N_ == 16 ? v ^ (v >> 1 & 1) : v; }
     float sX[kSsmTile * kX];                         // (delta, delta x, e, -), then (sum A p, sum G B, sum C h, -)
-    float sBC[BT * 2 * N_];                          // (B, B, C, C) of two states
+    using W = SsmWeights<T, NS / 2, LPC>;
+    float sBC[BT * W::kWords];                       // B and C
+    float sPar[2][CB];                               // dt_bias, D
+    float sAcc[2][kThreads][8];                      // dD, ddt_bias: a thread's sums over the tokens of its pieces
     float sRed[2][kWarps][BT * N_];                  // a warp's sums over its channels: dB, dC
     unsigned long long sEnt[EB / UG][NS / 2][kThreads];        // the state before each group
     unsigned long long sTop[EB < kSsmTile ? kSsmTile / EB : 1][NS / 2][kThreads];  // and before each EB tokens
 };
 
 template <typename T, int NS, int LPC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, float *__restrict__ pB, float *__restrict__ pC,
                     float *__restrict__ pA, float *__restrict__ pD, float *__restrict__ pbias) {
-    using M = BackMem<NS, LPC>;
+    using M = BackMem<T, NS, LPC>;
+    using W = typename M::W;
     constexpr int N_ = M::N_, NP = NS / 2, CB = M::CB, UG = M::UG, BT = M::BT, EB = M::EB, kX = M::kX, G_ = 32 / LPC;
     constexpr int PIECES = kSsmTile * CB / 8 / kThreads;    // (token, 8 channels) pieces per thread of a block
     extern __shared__ __align__(16) char smem_raw[];
@@ -83,6 +99,10 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
     const int nc = min(CB, cpg - c0), d0 = grp * cpg + c0;
     const bool on = ch < nc;
     const size_t ldx = a.channels, nstate = (size_t)a.channels * N_, own = (size_t)(d0 + (on ? ch : 0)) * N_ + q * NS;
+    int base = 0;  // the first of the 16 values whose sums over the warp's channels this lane ends up with
+#pragma unroll
+    for (int m = G_ / 2, n = 8; m > 0; m >>= 1, n >>= 1) base += lane / LPC & m ? n : 0;
+    const int red0 = M::slot(base / NS) * N_ + q * NS + base % NS, red1 = M::slot(base / NS + 1) * N_ + q * NS + base % NS;
     F2 A2[NP], A1[NP], r[NP], dA[NP];  // A log2 e, A, the gradient a_(t+1) G_(t+1) that comes in, dA
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
@@ -101,75 +121,40 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
     constexpr int TS = kThreads * 8 / CB;
     const int pt = tid % TS, pc = tid / TS * 8;
     const bool pon = pc < nc;
-    float bias[8], skip[8], dD[8], db[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = pon && a.dt_bias ? a.dt_bias[d0 + pc + i] : 0.f;
-        skip[i] = pon && a.D ? a.D[d0 + pc + i] : 0.f;
-        dD[i] = db[i] = 0.f;
+    // dt_bias and D by channel, and each thread's sums for dD and ddt_bias, kept out of the registers that the chain needs
+    if (tid < CB) {
+        sm.sPar[0][tid] = tid < nc && a.dt_bias ? a.dt_bias[d0 + tid] : 0.f;
+        sm.sPar[1][tid] = tid < nc && a.D ? a.D[d0 + tid] : 0.f;
     }
+    Pack8<float> zero;
+    zero.zero();
+#pragma unroll
+    for (int o = 0; o < 2; ++o) zero.store(sm.sAcc[o][tid]);
 
-    for (int64_t k = (e - b + kSsmTile - 1) / kSsmTile - 1; k >= 0; --k) {
+    // x, dt, dy, z of J of this thread's pieces (zeros behind the last token)
+    constexpr int J = PIECES < 2 ? 1 : 2;
+    Pack8<T> rows[J][4];
+    auto load_rows = [&](int64_t t0, int len, int u0) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int t = pt + (u0 + j) * TS;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rows[j][i].zero();
+            if (!pon || t >= len) continue;
+            const size_t at = (t0 + t) * ldx + pc;
+            rows[j][0].load(dt + at);
+            rows[j][1].load(x + at);
+            rows[j][2].load(dy + at);
+            if (z) rows[j][3].load(z + at);
+        }
+    };
+
+    constexpr int PK = (BT * N_ / 8 + kThreads - 1) / kThreads;
+    Pack8<T> nB[PK], nC[PK];  // the next stage's B and C,
+    int have = kSsmTile;      // of the tokens from this one on (none: kSsmTile)
+    for (int64_t k = (e - b + kSsmTile - 1) / kSsmTile - 1; k >= 0; --k, have += kSsmTile) {
         const int64_t t0 = b + k * kSsmTile;
         const int len = (int)min((int64_t)kSsmTile, e - t0);
-        __syncthreads();  // the block before has been read out
-#pragma unroll 1
-        for (int u = 0; u < PIECES; ++u) {
-            const int t = pt + u * TS;
-            if (t >= (len + UG - 1) / UG * UG) break;
-            float dl[8], xv[8], ev[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dl[i] = xv[i] = ev[i] = 0.f;
-            if (pon && t < len) {
-                Pack8<T> v;
-                const size_t at = (t0 + t) * ldx + pc;
-                v.load(dt + at);
-                v.get(dl);
-                v.load(x + at);
-                v.get(xv);
-                v.load(dy + at);
-                v.get(ev);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dl[i] += bias[i];
-                    if (a.softplus) dl[i] = softplus_f(dl[i]);
-                }
-                if (z) {
-                    float zv[8];
-                    v.load(z + at);
-                    v.get(zv);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) ev[i] *= silu_f(zv[i]);
-                }
-                // exp2_poly2's limits turn a NaN into a number: a step that is none goes into the chain here instead
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (dl[i] != dl[i]) ev[i] = dl[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float4 *>(sm.sX + t * kX + (pc + i) * 4) = make_float4(dl[i], dl[i] * xv[i], ev[i], 0.f);
-        }
-        auto stage = [&](int v0) {  // B and C of tokens v0 .. v0 + BT - 1 (zeros behind the last one)
-            for (int p = tid; p < BT * N_ / 8; p += kThreads) {
-                const int t = v0 + p / (N_ / 8);
-                float v[8], w[8];
-                Pack8<T> m;
-                m.zero();
-                if (t < len) m.load(Bp + (t0 + t) * ldb + (p % (N_ / 8)) * 8);
-                m.get(v);
-                m.zero();
-                if (t < len) m.load(Cp + (t0 + t) * ldb + (p % (N_ / 8)) * 8);
-                m.get(w);
-                float4 *to = reinterpret_cast<float4 *>(sm.sBC + p / (N_ / 8) * 2 * N_);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pair = p % (N_ / 8) * 4 + i;  // pair pair % NP of lane pair / NP
-                    to[pair % NP * LPC + pair / NP] = make_float4(v[2 * i], v[2 * i + 1], w[2 * i], w[2 * i + 1]);
-                }
-            }
-        };
-
         F2 h[NP];
         {
             const float *from = k == 0 ? a.S0 ? a.S0 + s * nstate : nullptr : a.tiles + (ssm_tile0(b, s) + k) * nstate;
@@ -179,12 +164,90 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
                 if (from) h[p].v = *reinterpret_cast<const unsigned long long *>(from + own + 2 * p);
             }
         }
+        load_rows(t0, len, 0);
+        if (k > 0) {  // the next block's rows into the L2 cache
+#pragma unroll
+            for (int u = 0; u < PIECES; ++u) {
+                const size_t at = (t0 - kSsmTile + pt + u * TS) * ldx + pc;
+                if (!pon) break;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(dt + at));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(x + at));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(dy + at));
+                if (z) asm volatile("prefetch.global.L2 [%0];" ::"l"(z + at));
+            }
+        }
+        __syncthreads();  // the block before has been read out
+#pragma unroll 1
+        for (int u0 = 0; u0 < PIECES; u0 += J) {
+            if (u0) load_rows(t0, len, u0);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int t = pt + (u0 + j) * TS;
+                if (t >= (len + UG - 1) / UG * UG) break;
+                float dl[8], xv[8], ev[8];
+                rows[j][0].get(dl);
+                rows[j][1].get(xv);
+                rows[j][2].get(ev);
+                if (pon && t < len) {
+                    float bias[8];
+                    Pack8<float> par;
+                    par.load(sm.sPar[0] + pc);
+                    par.get(bias);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dl[i] += bias[i];
+                        if (a.softplus) dl[i] = softplus_f(dl[i]);
+                    }
+                    if (z) {
+                        float zv[8];
+                        rows[j][3].get(zv);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) ev[i] *= silu_f(zv[i]);
+                    }
+                    // exp2_poly2's limits turn a NaN into a number: a step that is none goes into the chain here instead
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (dl[i] != dl[i]) ev[i] = dl[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<float4 *>(sm.sX + t * kX + (pc + i) * 4) = make_float4(dl[i], dl[i] * xv[i], ev[i], 0.f);
+            }
+        }
+        // B and C of the tokens v0 .. v0 + BT - 1 of this block (of the next one, where v0 < 0), zeros behind the last:
+        // loaded while the stage before is worked on, then put down
+        auto fetch = [&](int v0) {
+            if (t0 + v0 < b) return;
+            have = v0;
+#pragma unroll
+            for (int i = 0; i < PK; ++i) {
+                const int p = tid + i * kThreads, t = v0 + p / (N_ / 8);
+                nB[i].zero(), nC[i].zero();
+                if (p < BT * N_ / 8 && t < len) {
+                    const size_t at = (size_t)(t0 + t) * ldb + (p % (N_ / 8)) * 8;
+                    nB[i].load(Bp + at);
+                    nC[i].load(Cp + at);
+                }
+            }
+        };
+        auto stage = [&](int v0) {
+            if (have != v0) fetch(v0);
+#pragma unroll
+            for (int i = 0; i < PK; ++i) {
+                const int p = tid + i * kThreads;
+                if (p >= BT * N_ / 8) break;
+                W::put(sm.sBC + p / (N_ / 8) * W::kWords, p % (N_ / 8), nB[i], nC[i]);
+            }
+        };
+        auto behind = [&](int v0, int ta) { return v0 - BT >= ta ? v0 - BT : ta > 0 ? ta - EB : -kSsmTile; };  // the reverse order
+
         // forwards over the tokens [ta, tb); `keep`: the state before each group
         auto fold = [&](int ta, int tb, bool keep) {
 #pragma unroll 1
             for (int v0 = ta; v0 < tb; v0 += BT) {
                 __syncthreads();
                 stage(v0);
+                fetch(v0 + BT < tb || !keep ? v0 + BT : behind(v0, ta));
                 __syncthreads();
 #pragma unroll 1
                 for (int v = 0; v < BT && v0 + v < tb; v += UG) {
@@ -192,11 +255,12 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
 #pragma unroll
                     for (int u = 0; u < UG; ++u) {
                         const float2 w = *reinterpret_cast<const float2 *>(sm.sX + (v0 + v + u) * kX + ch * 4);
+                        F2 Cv[NP];
+                        W::get(sm.sBC + (v + u) * W::kWords, q, bv[u], Cv);
 #pragma unroll
                         for (int p = 0; p < NP; ++p) {
-                            const float2 m = *reinterpret_cast<const float2 *>(sm.sBC + (v + u) * 2 * N_ + (p * LPC + q) * 4);
                             av[u][p] = exp2_pair(mul2(f2(w.x, w.x), A2[p]));
-                            bv[u][p] = mul2(f2(w.y, w.y), f2(m.x, m.y));
+                            bv[u][p] = mul2(f2(w.y, w.y), bv[u][p]);
                         }
                     }
                     if (keep) {
@@ -230,6 +294,7 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
         for (int sb = subs - 1; sb >= ta / BT; --sb) {
             if (sb != subs - 1) {  // (the last one is still staged)
                 stage(sb * BT);
+                fetch(behind(sb * BT, ta));
                 __syncthreads();
             }
             const int groups = min((len - sb * BT + UG - 1) / UG, BT / UG);
@@ -242,11 +307,12 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
 #pragma unroll
                 for (int u = 0; u < UG; ++u) {
                     w[u] = *reinterpret_cast<const float4 *>(sm.sX + (t + u) * kX + ch * 4);
+                    F2 Cv[NP];
+                    W::get(sm.sBC + (v + u) * W::kWords, q, bv[u], Cv);
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
-                        const float2 m = *reinterpret_cast<const float2 *>(sm.sBC + (v + u) * 2 * N_ + (p * LPC + q) * 4);
                         av[u][p] = exp2_poly2(mul2(f2(w[u].x, w[u].x), A2[p]));
-                        bv[u][p] = mul2(f2(w[u].y, w[u].y), f2(m.x, m.y));
+                        bv[u][p] = mul2(f2(w[u].y, w[u].y), bv[u][p]);
                     }
                 }
 #pragma unroll
@@ -261,16 +327,16 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
 #pragma unroll
                 for (int u = UG - 1; u >= 0; --u) {
                     const F2 dl = f2(w[u].x, w[u].x), dx = f2(w[u].y, w[u].y), ev = f2(w[u].z, w[u].z);
-                    F2 tq = f2(0.f, 0.f), ts = tq, ty = tq;
+                    F2 tq = f2(0.f, 0.f), ts = tq, ty = tq, Bv[NP], Cv[NP];
+                    W::get(sm.sBC + (v + u) * W::kWords, q, Bv, Cv);
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
-                        const float4 m = *reinterpret_cast<const float4 *>(sm.sBC + (v + u) * 2 * N_ + (p * LPC + q) * 4);
-                        const F2 Bv = f2(m.x, m.y), Cv = f2(m.z, m.w), hv = add2(ah[u][p], bv[u][p]);
-                        const F2 Gv = fma2(Cv, ev, r[p]);
+                        const F2 hv = add2(ah[u][p], bv[u][p]);
+                        const F2 Gv = fma2(Cv[p], ev, r[p]);
                         const F2 pv = mul2(Gv, ah[u][p]);
-                        ty = p ? fma2(Cv, hv, ty) : mul2(Cv, hv);
+                        ty = p ? fma2(Cv[p], hv, ty) : mul2(Cv[p], hv);
                         tq = p ? fma2(A1[p], pv, tq) : mul2(A1[p], pv);
-                        ts = p ? fma2(Bv, Gv, ts) : mul2(Bv, Gv);
+                        ts = p ? fma2(Bv[p], Gv, ts) : mul2(Bv[p], Gv);
                         dA[p] = fma2(pv, dl, dA[p]);
                         vB[u][p] = mul2(Gv, dx);
                         vC[u][p] = mul2(hv, ev);
@@ -320,7 +386,6 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
                         unpack(vC[u][p], f[1][u * NS + 2 * p], f[1][u * NS + 2 * p + 1]);
                     }
                 const int c = lane / LPC;  // channel in the warp
-                int base = 0;
 #pragma unroll
                 for (int m = G_ / 2, n = 8; m > 0; m >>= 1, n >>= 1) {
                     const bool up = c & m;
@@ -331,22 +396,26 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
                             const float give = up ? f[o][i] : f[o][i + n], keep = up ? f[o][i + n] : f[o][i];
                             f[o][i] = keep + __shfl_xor_sync(0xffffffffu, give, m * LPC);
                         }
-                    base += up ? n : 0;
                 }
 #pragma unroll
-                for (int i = 0; i < 16 / G_; ++i) {
-                    const int at = (v + (base + i) / NS) * N_ + q * NS + (base + i) % NS;
-                    sm.sRed[0][warp][at] = f[0][i];
-                    sm.sRed[1][warp][at] = f[1][i];
+                for (int i = 0; i < 16 / G_; i += NS < 4 ? NS : 4) {
+                    const int at = v * N_ + (i / NS % 2 ? red1 : red0) + i / NS / 2 * 2 * N_ + i % NS;
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        float *to = sm.sRed[o][warp] + at;
+                        if constexpr (NS == 2) *reinterpret_cast<float2 *>(to) = make_float2(f[o][i], f[o][i + 1]);
+                        else *reinterpret_cast<float4 *>(to) = make_float4(f[o][i], f[o][i + 1], f[o][i + 2], f[o][i + 3]);
+                    }
                 }
             }
             __syncthreads();
             for (int i = tid; i < groups * UG * N_; i += kThreads) {
                 const int t = sb * BT + i / N_;
                 if (t >= len) break;
+                const int from = M::slot(i / N_) * N_ + i % N_;
                 float vb = 0.f, vc = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) vb += sm.sRed[0][w][i], vc += sm.sRed[1][w][i];
+                for (int w = 0; w < kWarps; ++w) vb += sm.sRed[0][w][from], vc += sm.sRed[1][w][from];
                 const size_t at = ((size_t)blk * a.total + t0 + t) * N_ + i % N_;
                 pB[at] = vb;
                 pC[at] = vc;
@@ -354,50 +423,60 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
             if (sb > ta / BT) __syncthreads();
         }
         }
+        load_rows(t0, len, 0);
         __syncthreads();
         // the rows' gradients
 #pragma unroll 1
-        for (int u = 0; u < PIECES; ++u) {
-            const int t = pt + u * TS;
-            if (!pon || t >= len) break;
-            const size_t at = (t0 + t) * ldx + pc;
-            Pack8<T> v;
-            float dtv[8], xv[8], dyv[8], o0[8], o1[8], o2[8], zv[8];
-            v.load(dt + at);
-            v.get(dtv);
-            v.load(x + at);
-            v.get(xv);
-            v.load(dy + at);
-            v.get(dyv);
-            if (z) {
-                v.load(z + at);
-                v.get(zv);
-            }
+        for (int u0 = 0; u0 < PIECES; u0 += J) {
+            if (u0) load_rows(t0, len, u0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 w = *reinterpret_cast<const float4 *>(sm.sX + t * kX + (pc + i) * 4);
-                const float raw = dtv[i] + bias[i], dl = a.softplus ? softplus_f(raw) : raw;
-                float ev = dyv[i];
-                if (z) {
-                    const float sg = sigmoid_f(zv[i]);
-                    o2[i] = dyv[i] * fmaf(skip[i], xv[i], w.z) * sg * fmaf(zv[i], 1.f - sg, 1.f);
-                    ev *= zv[i] * sg;
+            for (int j = 0; j < J; ++j) {
+                const int t = pt + (u0 + j) * TS;
+                if (!pon || t >= len) break;
+                const size_t at = (t0 + t) * ldx + pc;
+                float dtv[8], xv[8], dyv[8], o0[8], o1[8], o2[8], zv[8], bias[8], skip[8], dD[8], db[8];
+                Pack8<float> w;
+                w.load(sm.sPar[0] + pc);
+                w.get(bias);
+                w.load(sm.sPar[1] + pc);
+                w.get(skip);
+                w.load(sm.sAcc[0][tid]);
+                w.get(dD);
+                w.load(sm.sAcc[1][tid]);
+                w.get(db);
+                rows[j][0].get(dtv);
+                rows[j][1].get(xv);
+                rows[j][2].get(dyv);
+                rows[j][3].get(zv);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 w = *reinterpret_cast<const float4 *>(sm.sX + t * kX + (pc + i) * 4);
+                    const float raw = dtv[i] + bias[i], dl = a.softplus ? softplus_f(raw) : raw;
+                    float ev = dyv[i];
+                    if (z) {
+                        const float sg = sigmoid_f(zv[i]);
+                        o2[i] = dyv[i] * fmaf(skip[i], xv[i], w.z) * sg * fmaf(zv[i], 1.f - sg, 1.f);
+                        ev *= zv[i] * sg;
+                    }
+                    o0[i] = fmaf(dl, w.y, skip[i] * ev);
+                    const float dd = fmaf(xv[i], w.y, w.x);
+                    o1[i] = a.softplus ? dd * sigmoid_f(raw) : dd;
+                    dD[i] = fmaf(ev, xv[i], dD[i]);
+                    db[i] += o1[i];
                 }
-                o0[i] = fmaf(dl, w.y, skip[i] * ev);
-                const float dd = fmaf(xv[i], w.y, w.x);
-                o1[i] = a.softplus ? dd * sigmoid_f(raw) : dd;
-                dD[i] = fmaf(ev, xv[i], dD[i]);
-                db[i] += o1[i];
-            }
-            Pack8<float> w;
-            const size_t to = at + d0;
-            w.set(o0);
-            w.store_stream(g.dx + to);
-            w.set(o1);
-            w.store_stream(g.ddt + to);
-            if (z) {
-                w.set(o2);
-                w.store_stream(g.dz + to);
+                w.set(dD);
+                w.store(sm.sAcc[0][tid]);
+                w.set(db);
+                w.store(sm.sAcc[1][tid]);
+                const size_t to = at + d0;
+                w.set(o0);
+                w.store_stream(g.dx + to);
+                w.set(o1);
+                w.store_stream(g.ddt + to);
+                if (z) {
+                    w.set(o2);
+                    w.store_stream(g.dz + to);
+                }
             }
         }
     }
@@ -410,18 +489,10 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
     }
     // dD, ddt_bias: the sums of the threads that share 8 channels, in the order of their tokens
     __syncthreads();
-    float *red = sm.sX;  // [2][8][kThreads]
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        red[i * kThreads + tid] = dD[i];
-        red[(8 + i) * kThreads + tid] = db[i];
-    }
-    __syncthreads();
     for (int i = tid; i < 2 * nc; i += kThreads) {
         const int c = i % nc;
-        const float *from = red + ((i / nc) * 8 + c % 8) * kThreads + c / 8 * TS;
         float v = 0.f;
-        for (int t = 0; t < TS; ++t) v += from[t];
+        for (int t = 0; t < TS; ++t) v += sm.sAcc[i / nc][c / 8 * TS + t][c % 8];
         (i < nc ? pD : pbias)[(size_t)s * ldx + d0 + c] = v;
     }
 }
@@ -497,7 +568,7 @@ cudaError_t launch_back(const SsmBackwardArgs &g, cudaStream_t st) {
     const size_t rows = (size_t)nblk * a.total * a.states, nA = (size_t)a.N * a.channels * a.states;
     float *pB = static_cast<float *>(g.ws), *pC = pB + rows, *pA = pC + rows, *pD = pA + nA, *pb = pD + (size_t)a.N * a.channels;
     auto kern = ssm_backward_kernel<T, NS, LPC>;
-    constexpr int bytes = sizeof(BackMem<NS, LPC>);
+    constexpr int bytes = sizeof(BackMem<T, NS, LPC>);
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); e != cudaSuccess) return e;
     kern<<<(unsigned)((int64_t)a.N * nblk), kThreads, bytes, st>>>(g, nblk, bpg, pB, pC, pA, pD, pb);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
