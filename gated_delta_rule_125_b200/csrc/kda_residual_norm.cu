@@ -11,8 +11,9 @@
 //
 // Bound by memory: every row is read once and stays in registers through its two (three) row sums. A
 // CTA takes a row at a time, one vector of 8 channels per thread (two above 4096 channels), and loads the
-// next row before it works on the current one. The column sums of the backward stay in each thread's registers over all
-// of its CTA's rows; one partial row per CTA goes to the workspace and norm_sum_kernel adds them in order.
+// next row before it works on the current one. The column sums of the backward stay in shared memory, each
+// thread's its own, over all of its CTA's rows; one partial row per CTA goes to the workspace and
+// norm_sum_kernel adds them in order.
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -68,6 +69,17 @@ template <typename T, typename R, int V> struct Row {
             if (a.r) r[k].load_stream(static_cast<const R *>(a.r) + at);
         }
     }
+    __device__ __forceinline__ float squares() const {  // this thread's part of the row's sum of y^2
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            float v[8];
+            y[k].get(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
+        }
+        return s;
+    }
 };
 
 template <typename T, typename R, int V, int THREADS>
@@ -84,13 +96,7 @@ norm_kernel(const NormArgs a) {
         if (kAhead) next.load(a, row + gridDim.x);
         float out[V][8], sum[1] = {0.f};
         if (a.w_post) {
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                float y[8];
-                in.y[k].get(y);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[0] = fmaf(y[i], y[i], sum[0]);
-            }
+            sum[0] = in.squares();
             row_sums(sum, red, 0);
         }
         const float rs1 = rsqrtf(fmaf(sum[0], inv, a.eps));
@@ -152,11 +158,38 @@ norm_backward_kernel(const NormBackwardArgs p, float *__restrict__ part) {
     const NormArgs &a = p.f;
     __shared__ float red[3][2][kMaxThreads / 32];
     const float inv = 1.f / a.D;
-    float d_post[V][8], d_scale[V][8], d_pre[V][8];
+    // this thread's column sums (w_post, scale, w_pre) lie in shared memory: the registers hold its weights (V = 1)
+    extern __shared__ __align__(16) char smem_raw[];
+    float4 *mine = reinterpret_cast<float4 *>(smem_raw) + threadIdx.x;
+    auto sum_of = [&](int j, int k, int half) -> float4 & { return mine[((j * V + k) * 2 + half) * blockDim.x]; };
+    auto add = [&](int j, int k, const float (&x)[8], const float (&y)[8]) {
 #pragma unroll
-    for (int k = 0; k < V; ++k)
+        for (int half = 0; half < 2; ++half) {
+            float4 v = sum_of(j, k, half);
+            v.x = fmaf(x[4 * half], y[4 * half], v.x), v.y = fmaf(x[4 * half + 1], y[4 * half + 1], v.y);
+            v.z = fmaf(x[4 * half + 2], y[4 * half + 2], v.z), v.w = fmaf(x[4 * half + 3], y[4 * half + 3], v.w);
+            sum_of(j, k, half) = v;
+        }
+    };
+    float wr[V == 1 ? 3 : 1][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d_post[k][i] = d_scale[k][i] = d_pre[k][i] = 0.f;
+    for (int k = 0; k < 6 * V; ++k) mine[k * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (V == 1) {
+        const int cc = min((int)threadIdx.x * 8, a.D - 8);
+        load_weights(a.scale, cc, wr[0], 1.f);
+        load_weights(a.w_post, cc, wr[1], 1.f);
+        load_weights(a.w_pre, cc, wr[2], 0.f);
+    }
+    auto weights = [&](int cc, float (&s)[8], float (&w)[8], float (&q)[8]) {
+        if constexpr (V == 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = wr[0][i], w[i] = wr[1][i], q[i] = wr[2][i];
+        } else {
+            load_weights(a.scale, cc, s, 1.f);
+            load_weights(a.w_post, cc, w, 1.f);
+            load_weights(a.w_pre, cc, q, 0.f);
+        }
+    };
     Row<T, R, V> next;
     Pack8<T> ndx[V];
     Pack8<float> ndr[V];
@@ -172,7 +205,14 @@ norm_backward_kernel(const NormBackwardArgs p, float *__restrict__ part) {
             if (p.dr_out) ndr[k].load_stream(p.dr_out + at);
         }
     };
-    if (V == 1) load(blockIdx.x);
+    float y2[1] = {0.f};
+    if (V == 1) {
+        load(blockIdx.x);
+        if (a.w_post) {
+            y2[0] = next.squares();
+            row_sums(y2, red, 0);
+        }
+    }
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         if (V > 1) load(row);
         const Row<T, R, V> in = next;
@@ -183,18 +223,11 @@ norm_backward_kernel(const NormBackwardArgs p, float *__restrict__ part) {
             ndx[k].get(h[k]);
         }
         if (V == 1) load(row + gridDim.x);
-        float sum[1] = {0.f};
-        if (a.w_post) {
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                float y[8];
-                in.y[k].get(y);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[0] = fmaf(y[i], y[i], sum[0]);
-            }
-            row_sums(sum, red, 0);
+        if (V > 1 && a.w_post) {
+            y2[0] = in.squares();
+            row_sums(y2, red, 0);
         }
-        const float rs1 = rsqrtf(fmaf(sum[0], inv, a.eps));
+        const float rs1 = rsqrtf(fmaf(y2[0], inv, a.eps));
         float two[2] = {0.f, 0.f}, out[V][8];  // sums of r'^2 and w_pre dx r'
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -203,9 +236,7 @@ norm_backward_kernel(const NormBackwardArgs p, float *__restrict__ part) {
             in.y[k].get(y);
             in.g[k].get(g);
             in.r[k].get(r);
-            load_weights(a.scale, cc, s, 1.f);
-            load_weights(a.w_post, cc, w, 1.f);
-            load_weights(a.w_pre, cc, q, 0.f);
+            weights(cc, s, w, q);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float u = y[i];
@@ -222,21 +253,21 @@ norm_backward_kernel(const NormBackwardArgs p, float *__restrict__ part) {
             rs2 = rsqrtf(fmaf(two[0], inv, a.eps));
             mean = two[1] * inv * rs2 * rs2;
         }
-        sum[0] = 0.f;
+        float sum[2] = {0.f, 0.f};  // of w_post f y; of the next row's y^2 (V = 1), one exchange for both
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int c = (threadIdx.x + k * blockDim.x) * 8, cc = min(c, a.D - 8);
             const bool on = c < a.D;
             const size_t at = (size_t)row * a.D + c;
-            float y[8], g[8], w[8], s[8], q[8], o[8];
+            float y[8], g[8], w[8], s[8], q[8], o[8], e[8];
             in.y[k].get(y);
             in.g[k].get(g);
-            load_weights(a.scale, cc, s, 1.f);
-            load_weights(a.w_post, cc, w, 1.f);
-            load_weights(a.w_pre, cc, q, 0.f);
+            weights(cc, s, w, q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = out[k][i] * rs2;
+            add(2, k, h[k], e);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                d_pre[k][i] = fmaf(h[k][i], out[k][i] * rs2, d_pre[k][i]);
                 d[k][i] = fmaf(rs2, fmaf(-out[k][i], mean, h[k][i] * q[i]), d[k][i]);
                 o[i] = a.res_scale * d[k][i];
             }
@@ -249,14 +280,19 @@ norm_backward_kernel(const NormBackwardArgs p, float *__restrict__ part) {
             for (int i = 0; i < 8; ++i) {
                 const float u = a.w_post ? y[i] * rs1 * w[i] : y[i];
                 const float m = a.gate ? sigmoid_f(g[i]) : 1.f;
-                d_scale[k][i] = fmaf(d[k][i], m * u, d_scale[k][i]);
+                e[i] = m * u;
+                out[k][i] = d[k][i];
                 const float ds = d[k][i] * s[i];
                 o[i] = ds * u * m * (1.f - m);
                 const float f = ds * m;
-                d_post[k][i] = fmaf(f, y[i] * rs1, d_post[k][i]);
+                h[k][i] = f;
                 d[k][i] = a.w_post ? f * w[i] : f;  // w_post f
                 sum[0] = fmaf(d[k][i], y[i], sum[0]);
             }
+            add(1, k, out[k], e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = y[i] * rs1;
+            add(0, k, h[k], e);
             if (on && a.gate) {
                 v.set(o);
                 v.store_stream(p.dgate + at);
@@ -264,8 +300,11 @@ norm_backward_kernel(const NormBackwardArgs p, float *__restrict__ part) {
         }
         float back = 0.f;
         if (a.w_post) {
+            if (V == 1) sum[1] = next.squares();
             row_sums(sum, red, 2);
             back = sum[0] * inv * rs1 * rs1;
+            if (V == 1) y2[0] = sum[1];
+            if (!a.w_pre) __syncthreads();  // (the next row's sums take the same slot)
         } else {
             __syncthreads();  // the next row's sum takes the slot that this row's readers may still read
         }
@@ -288,13 +327,10 @@ norm_backward_kernel(const NormBackwardArgs p, float *__restrict__ part) {
         const int c = (threadIdx.x + k * blockDim.x) * 8;
         if (c >= a.D) continue;
         float *to = part + (size_t)blockIdx.x * 3 * a.D + c;
-        Pack8<float> v;
-        v.set(d_post[k]);
-        v.store(to);
-        v.set(d_scale[k]);
-        v.store(to + a.D);
-        v.set(d_pre[k]);
-        v.store(to + 2 * a.D);
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) *reinterpret_cast<float4 *>(to + j * a.D + 4 * half) = sum_of(j, k, half);
     }
 }
 
@@ -342,8 +378,11 @@ template <typename T, typename R> cudaError_t launch(const NormArgs &a, cudaStre
     return cudaGetLastError();
 }
 
-// Backward: 512 threads, one vector each up to 4096 channels, one CTA to an SM (219 us for 8191 rows of 4096
-// channels, its stream in fp32, 61 % of the copy rate; 256 threads of two vectors, two CTAs: 236 us).
+// Backward: 512 threads, one vector each up to 4096 channels, one CTA to an SM: 165 us for 8191 rows of 4096
+// channels, its stream in fp32, 81 % of the copy rate. With the column sums in registers and the weights read
+// again for every row 218 us (256 threads of two vectors, two CTAs: 236 us); with the sum of y^2 exchanged by
+// itself, not together with the row before's last sum, 181 us. (The forward, three CTAs to an SM, loses by
+// that: 63 us against 60, it waits for the next row's loads.)
 unsigned back_ctas(int64_t rows, int D) {
     return (unsigned)ctas_of(rows, threads_of(D, kMaxThreads), kMaxThreads, 1);
 }
@@ -352,8 +391,10 @@ template <typename T, typename R> cudaError_t launch_back(const NormBackwardArgs
     const int nt = threads_of(a.D, kMaxThreads);
     const unsigned grid = back_ctas(a.rows, a.D);
     float *part = static_cast<float *>(p.ws);
-    if (a.D <= 8 * kMaxThreads) norm_backward_kernel<T, R, 1><<<grid, nt, 0, st>>>(p, part);
-    else norm_backward_kernel<T, R, 2><<<grid, nt, 0, st>>>(p, part);
+    auto kern = a.D <= 8 * kMaxThreads ? norm_backward_kernel<T, R, 1> : norm_backward_kernel<T, R, 2>;
+    const int bytes = 3 * 2 * (int)sizeof(float4) * nt * (a.D <= 8 * kMaxThreads ? 1 : 2);
+    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); e != cudaSuccess) return e;
+    kern<<<grid, nt, bytes, st>>>(p, part);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     if (p.dw_post || p.dscale || p.dw_pre)
         norm_sum_kernel<<<dim3((a.D + 31) / 32, 3), 256, 0, st>>>(part, (int)grid, a.D, p.dw_post, p.dscale, p.dw_pre);
