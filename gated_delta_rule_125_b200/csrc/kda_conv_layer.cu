@@ -9,8 +9,10 @@
 //
 // All of it is bound by memory: x (and dy) read once, y (dx) written once. A thread owns 4 consecutive
 // channels of a run of consecutive tokens and keeps the window in registers (8 channels halve the loads and
-// double the registers: 117 us against 85 us for the backward of 8192 tokens x 4096 channels, W = 4).
-// It loads some rows ahead, so that enough bytes are in flight. The rows around its run that its
+// double the registers: 117 us against 85 us for an earlier backward of 8192 tokens x 4096 channels, W = 4).
+// It loads some rows ahead, so that enough bytes are in flight: the forward (32 us for that size, 64 % of the
+// copy rate, its exponentials and reciprocals at 54 % of theirs) to registers, the backward, which has none left,
+// to shared memory (60 us, 68 %; to registers and none further ahead 85 us). The rows around its run that its
 // window needs are its neighbours' too and come from the L2 cache.
 #include <type_traits>
 
@@ -72,6 +74,7 @@ template <int V> __device__ __forceinline__ void load_bias(const float *bias, in
 
 constexpr int kRun = 32, kVec = 4;                         // tokens and channels of a thread's run
 constexpr int ahead(int W) { return W > 4 ? 1 : 4; }       // rows loaded together (wide windows take the registers)
+constexpr int ring(int W) { return W > 4 ? 8 : 2; }        // such groups in the backward's ring (three: 62 us, not 60)
 
 template <int W, int V, typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -210,14 +213,17 @@ conv_step_kernel(const ConvArgs a) {
 // and conv_sum_kernel adds the runs in order. A sequence's dstate is written by the thread of its first
 // token, which holds the g of its first W - 1 tokens.
 
-// Long runs cost less (a row of partial sums each, W - 1 tokens formed twice), short ones fill the GPU:
-// 128 tokens where that leaves a thread for every lane of two CTAs per SM, else 32.
-int back_run(int64_t total, int C) { return total / 128 * (C / kVec) >= 148 * 2 * kThreads ? 128 : 32; }
+// Long runs cost less (a row of partial sums each, W - 1 tokens formed twice), short ones fill the GPU: as
+// long as leaves a thread for every lane of four CTAs per SM, at least 32 tokens.
+int back_run(int64_t total, int C) {
+    const int64_t runs = max((int64_t)148 * 4 * kThreads * kVec / C, (int64_t)1);
+    return (int)max(((total + runs - 1) / runs + 3) / 4 * 4, (int64_t)32);
+}
 
 template <int W, int V, typename T, typename TG>
 __global__ void __launch_bounds__(kThreads, W <= 4 ? 4 : 1)
 conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part, const int run_len) {
-    constexpr int kAhead = ahead(W);
+    constexpr int kAhead = ahead(W), kRing = ring(W);
     const ConvArgs &a = p.f;
     const int nv = a.C / V;
     const int64_t gid = (int64_t)blockIdx.x * kThreads + threadIdx.x, run = gid / nv, t0 = run * run_len;
@@ -227,6 +233,8 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part, const i
     const T *x = static_cast<const T *>(a.x) + c0;
     const T *st = a.state_in ? static_cast<const T *>(a.state_in) + c0 : nullptr;
     const TG *dy = static_cast<const TG *>(p.dy) + c0;
+    __shared__ Pack<T, V> ring_x[kRing * kAhead][kThreads];
+    __shared__ Pack<TG, V> ring_dy[kRing * kAhead][kThreads];
     float tap[W][V], bias[V], dw[W][V], db[V];
     load_taps<W, V>(a.w, c0, tap);
     load_bias(a.bias, c0, bias);
@@ -259,26 +267,29 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part, const i
                 o.store(p.dstate + ((size_t)s * (W - 1) + (t - b + W - 1)) * a.C + c0);
             }
         };
-        start(t0);
-        // n tokens of the current sequence from t on (`inner`: kAhead of them, in the run, and so are the rows whose dx
-        // they complete)
-        auto tokens = [&](auto inner, int64_t t, int n) {
-            constexpr bool kInner = decltype(inner)::value;
-            const T *px = x + (size_t)t * a.C;
-            const TG *pg = dy + (size_t)t * a.C;
-            float *pd = p.dx + (size_t)(t - (W - 1)) * a.C + c0;
-            Pack<T, V> nx[kAhead];
-            Pack<TG, V> ny[kAhead];
+        // x and dy come through a ring of kRing groups of kAhead rows, each thread's its own (no barrier)
+        auto copy = [&](int64_t t, int at) {
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k, px += a.C, pg += a.C) {
-                if (!kInner && k >= n) break;
-                nx[k].load(px);
-                ny[k].load(pg);
+            for (int k = 0; k < kAhead; ++k) {
+                if (t + k >= tl) break;
+                copy_pack(&ring_x[at + k][threadIdx.x], x + (size_t)(t + k) * a.C);
+                copy_pack(&ring_dy[at + k][threadIdx.x], dy + (size_t)(t + k) * a.C);
             }
+            copies_end_group();
+        };
+#pragma unroll
+        for (int i = 0; i < kRing - 1; ++i) copy(t0 + i * kAhead, i * kAhead);
+        int head = 0;  // the current group's place
+        start(t0);
+        // n tokens of the current sequence from t on, in one group, the rows from `at` on of the ring (`inner`: kAhead of
+        // them, in the run, and so are the rows whose dx they complete)
+        auto tokens = [&](auto inner, int64_t t, int n, int at) {
+            constexpr bool kInner = decltype(inner)::value;
+            float *pd = p.dx + (size_t)(t - (W - 1)) * a.C + c0;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k, pd += a.C) {
                 if (!kInner && k >= n) break;
-                nx[k].get(win[W - 1]);
+                ring_x[at + k][threadIdx.x].get(win[W - 1]);
                 float v[V], g[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -290,7 +301,7 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part, const i
 #pragma unroll
                     for (int i = 0; i < V; ++i) v[i] = fmaf(tap[j][i], win[j][i], v[i]);
                 }
-                ny[k].get(g);
+                ring_dy[at + k][threadIdx.x].get(g);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const float sg = sigmoid_f(v[i]);
@@ -340,11 +351,18 @@ conv_backward_kernel(const ConvBackwardArgs p, float *__restrict__ part, const i
                 } while (e == b);
                 start(t);
             }
-            const int n = (int)min((int64_t)kAhead, min(tl, e) - t);
-            if (n == kAhead && t - (W - 1) >= max(b, t0) && t + kAhead <= t1) tokens(std::true_type{}, t, n);
-            else tokens(std::false_type{}, t, n);
+            const int in = (int)(t - t0) % kAhead;
+            if (in == 0) {
+                copy(t + (kRing - 1) * kAhead, (head + (kRing - 1) * kAhead) % (kRing * kAhead));
+                copies_wait<kRing - 1>();
+            }
+            const int n = (int)min((int64_t)(kAhead - in), min(tl, e) - t);
+            if (n == kAhead && t - (W - 1) >= max(b, t0) && t + kAhead <= t1) tokens(std::true_type{}, t, n, head);
+            else tokens(std::false_type{}, t, n, head + in);
             t += n;
+            if (in + n == kAhead) head = (head + kAhead) % (kRing * kAhead);
         }
+        copies_wait<0>();
         if (e >= 0) {  // what is left: rows up to the last of the run (complete: their sequence, or the rows, end here)
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)

@@ -110,6 +110,13 @@ __device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.comm
 template <int N> __device__ __forceinline__ void copies_wait() {  // until at most the N last groups are in flight
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// Four channels likewise (`to`: a place that only this thread reads).
+template <typename P, typename T> __device__ __forceinline__ void copy_pack(P *to, const T *from) {
+    static_assert(sizeof(P) == 8 || sizeof(P) == 16, "bytes");
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (sizeof(P) == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
+    else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+}
 // Eight channels by copy16, to a place that only this thread reads.
 template <typename T> __device__ __forceinline__ void copy8(Pack8<T> *to, const T *from, bool on) {
 #pragma unroll

@@ -497,8 +497,8 @@ kda_status kda_short_conv_step(const void *x, void *y, const kda_short_conv *con
  *
  * Rows from cu_seqlens[N] on are neither read nor written. dweight and dbias are summed in a fixed
  * order (no atomics). dx must not overlap x or dy (KDA_ERR_INVALID_ARG), no output may overlap an input.
- * workspace: kda_short_conv_backward_workspace_size() bytes (a partial dweight and dbias per 128 tokens,
- * per 32 for calls that 128 would not fill the GPU with). Two launches, three with dstate and cu_seqlens.
+ * workspace: kda_short_conv_backward_workspace_size() bytes (a partial dweight and dbias per 32 tokens, or
+ * per longer runs where those fill the GPU). Two launches, three with dstate and cu_seqlens.
  */
 size_t kda_short_conv_backward_workspace_size(int64_t total_tokens, int32_t channels, int32_t width);
 kda_status kda_short_conv_backward(const void *x, const kda_short_conv *conv, const float *bias,
