@@ -213,10 +213,12 @@ conv_step_kernel(const ConvArgs a) {
 // and conv_sum_kernel adds the runs in order. A sequence's dstate is written by the thread of its first
 // token, which holds the g of its first W - 1 tokens.
 
-// Long runs cost less (a row of partial sums each, W - 1 tokens formed twice), short ones fill the GPU: as
-// long as leaves a thread for every lane of four CTAs per SM, at least 32 tokens.
+// Long runs cost less (a row of partial sums each, W - 1 tokens formed twice), short ones fill the GPU: runs
+// that give every lane of four CTAs per SM one each, or as many each as keep them at 128 tokens (whose sums
+// keep their bits), and at least 32 tokens (8192 tokens x 4096 channels: runs of 128, 64 of 74, 67 us).
 int back_run(int64_t total, int C) {
-    const int64_t runs = max((int64_t)148 * 4 * kThreads * kVec / C, (int64_t)1);
+    const int64_t lanes = max((int64_t)148 * 4 * kThreads * kVec / C, (int64_t)1);
+    const int64_t runs = max((total + 128 * lanes - 1) / (128 * lanes), (int64_t)1) * lanes;
     return (int)max(((total + runs - 1) / runs + 3) / 4 * 4, (int64_t)32);
 }
 

@@ -103,13 +103,14 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
 #pragma unroll
     for (int m = G_ / 2, n = 8; m > 0; m >>= 1, n >>= 1) base += lane / LPC & m ? n : 0;
     const int red0 = M::slot(base / NS) * N_ + q * NS + base % NS, red1 = M::slot(base / NS + 1) * N_ + q * NS + base % NS;
-    F2 A2[NP], A1[NP], r[NP], dA[NP];  // A log2 e, A, the gradient a_(t+1) G_(t+1) that comes in, dA
+    F2 A2[NP], A1[NP], r[NP];  // A log2 e, A, the gradient a_(t+1) G_(t+1) that comes in
+    F2 dA[NP], blockA[NP];     // dA of the blocks done, of this one (added group by group: short sums keep their bits)
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const float2 v = *reinterpret_cast<const float2 *>(a.A + own + 2 * p);
         A1[p] = f2(v.x, v.y);
         A2[p] = f2(v.x * kLog2e, v.y * kLog2e);
-        r[p] = dA[p] = f2(0.f, 0.f);
+        r[p] = dA[p] = blockA[p] = f2(0.f, 0.f);
         if (g.dS_T && on) r[p].v = *reinterpret_cast<const unsigned long long *>(g.dS_T + s * nstate + own + 2 * p);
     }
     const T *x = static_cast<const T *>(a.x) + d0, *dt = static_cast<const T *>(a.dt) + d0;
@@ -303,6 +304,7 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
                 const int t = sb * BT + v;
                 F2 av[UG][NP], ah[UG][NP], bv[UG][NP], vB[UG][NP], vC[UG][NP];
                 float4 w[UG];
+                F2 groupA[NP];
                 float sq[UG], ss[UG], sy[UG];
 #pragma unroll
                 for (int u = 0; u < UG; ++u) {
@@ -337,7 +339,7 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
                         ty = p ? fma2(Cv[p], hv, ty) : mul2(Cv[p], hv);
                         tq = p ? fma2(A1[p], pv, tq) : mul2(A1[p], pv);
                         ts = p ? fma2(Bv[p], Gv, ts) : mul2(Bv[p], Gv);
-                        dA[p] = fma2(pv, dl, dA[p]);
+                        groupA[p] = u == UG - 1 ? mul2(pv, dl) : fma2(pv, dl, groupA[p]);
                         vB[u][p] = mul2(Gv, dx);
                         vC[u][p] = mul2(hv, ev);
                         r[p] = mul2(av[u][p], Gv);
@@ -350,6 +352,8 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
                     unpack(ty, lo, hi);
                     sy[u] = lo + hi;
                 }
+#pragma unroll
+                for (int p = 0; p < NP; ++p) blockA[p] = add2(blockA[p], groupA[p]);
                 // over the channel's lanes: lane q keeps the tokens u = q mod UG
 #pragma unroll
                 for (int m = LPC / 2; m > 0; m >>= 1) {
@@ -422,6 +426,11 @@ ssm_backward_kernel(const SsmBackwardArgs g, const int nblk, const int bpg, floa
             }
             if (sb > ta / BT) __syncthreads();
         }
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            dA[p] = add2(dA[p], blockA[p]);
+            blockA[p] = f2(0.f, 0.f);
         }
         load_rows(t0, len, 0);
         __syncthreads();
@@ -550,8 +559,13 @@ ssm_param_kernel(const int N, const int channels, const int states, const float 
     }
     if (!to) return;
     float v = 0.f;
+    for (int s0 = 0; s0 < N; s0 += 64) {  // 64 at a time: short sums keep their bits
+        float part = 0.f;
+        const int s1 = min(s0 + 64, N);
 #pragma unroll 8
-    for (int s = 0; s < N; ++s) v += from[s * ld + i];
+        for (int s = s0; s < s1; ++s) part += from[s * ld + i];
+        v += part;
+    }
     to[i] = v;
 }
 
