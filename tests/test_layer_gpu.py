@@ -561,6 +561,29 @@ def test_conv_backward(lengths, C, W, dtype, dy_dtype):
     within(again[0], L.conv_backward(h["x"], h["w"], host(dy), h["cu"])[0], mdx, chain, "dx without bias")
 
 
+def test_conv_backward_long_runs():
+    """Wide calls take longer runs of tokens than narrow ones: the same dx and dstate to the bit, and column sums that
+    differ by the order of their additions alone (at most 128 in a run and 30 over the runs here, 32 and 46 there)."""
+    lengths, C, W = [3000, 2, 0, 5190, 1408], 4096, 4
+    T = sum(lengths)
+    k = conv_case(lengths, C, W, BF16, seed=12)
+    dy = randn(T, C, seed=13, dtype=BF16)
+    wide = kda.kda_short_conv_backward(k["x"], k["w"], dy, k["cu"], bias=k["bias"], state_in=k["state"], want_dstate=True)
+    for c in (slice(0, 16), slice(2040, 2056), slice(C - 16, C)):
+        part = {n: k[n][..., c].contiguous() for n in ("x", "state", "bias")}
+        part["w"] = k["w"][c].contiguous()
+        dyc = dy[:, c].contiguous()
+        dx, dw, db, ds = kda.kda_short_conv_backward(part["x"], part["w"], dyc, k["cu"], bias=part["bias"], state_in=part["state"],
+                                                     want_dstate=True)
+        assert torch.equal(wide[0][:, c], dx) and torch.equal(wide[3][..., c], ds)
+        g, mag = 1.1 * np.abs(host(dyc)), np.zeros((16, W))
+        for s, b, e, rows in L._windows(np.abs(host(part["x"])), W, k["cu"].cpu().numpy(), np.abs(host(part["state"]))):
+            for j in range(W):
+                mag[:, j] += (g[b:e] * rows[j:j + e - b]).sum(0)
+        assert (np.abs(host(wide[1][c]) - host(dw)) <= 236 * 2.0 ** -24 * mag).all()
+        assert (np.abs(host(wide[2][c]) - host(db)) <= 236 * 2.0 ** -24 * g.sum(0)).all()
+
+
 def test_conv_rows_behind_the_last_sequence():
     k = conv_case([50, 20], 16, 4, F32, seed=6)
     x = torch.cat([k["x"], torch.full((130, 16), float("nan"), device=DEV)])
