@@ -380,9 +380,9 @@ ssm_join_kernel(const SsmArgs a, const int L, float *__restrict__ seg_state, con
 
 // How the lanes and the time axis are dealt out.
 constexpr int kMinSegment = 256;
-// Lanes of a channel. 16 states: four lanes 381 us for 8192 tokens of 4096 channels, eight 423 us (fewer
-// shuffles against more warps). 64 states: eight lanes 177 us for 6151 tokens of 1024 channels in 16
-// sequences, sixteen 221 us.
+// Lanes of a channel (on one GPU). 16 states: four lanes 342 us for 8192 tokens of 4096 channels, eight 355 us
+// (fewer shuffles against more warps). 64 states: eight lanes 158 us for 6151 tokens of 1024 channels in 16
+// sequences, sixteen 225 us.
 constexpr int lanes_of(int states) { return states <= 16 ? 4 : 8; }
 struct Cut {
     int L;  // tokens of a segment
@@ -391,7 +391,7 @@ struct Cut {
     bool split;
 };
 // The time axis is cut where the sequences' channels give a CTA to fewer than half of the SMs: a cut takes
-// the exponentials twice (8192 tokens of 4096 channels, 128 CTAs: 381 us uncut, 531 us in four segments).
+// the exponentials twice (8192 tokens of 4096 channels, 128 CTAs: 342 us uncut, 420 us in four segments).
 Cut cut_of(int64_t total, int N, int channels, int states, int groups) {
     const int CB = kScanThreads / lanes_of(states);
     Cut c;
