@@ -263,14 +263,15 @@ norm_backward_kernel(const NormBackwardArgs p, float *__restrict__ part) {
             in.y[k].get(y);
             in.g[k].get(g);
             weights(cc, s, w, q);
+            if (a.w_pre) {  // without it d = dr', whatever r' holds (0 times an infinite r' would be a NaN)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = out[k][i] * rs2;
-            add(2, k, h[k], e);
+                for (int i = 0; i < 8; ++i) e[i] = out[k][i] * rs2;
+                add(2, k, h[k], e);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                d[k][i] = fmaf(rs2, fmaf(-out[k][i], mean, h[k][i] * q[i]), d[k][i]);
-                o[i] = a.res_scale * d[k][i];
+                for (int i = 0; i < 8; ++i) d[k][i] = fmaf(rs2, fmaf(-out[k][i], mean, h[k][i] * q[i]), d[k][i]);
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = a.res_scale * d[k][i];
             Pack8<float> v;
             if (on && p.dr) {
                 v.set(o);

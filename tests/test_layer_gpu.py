@@ -722,6 +722,25 @@ def test_residual_norm_many_rows_same_bits():
     assert (g.dw_pre == 0).all() and (g.dscale == 0).all()
 
 
+@pytest.mark.parametrize("dtype,res", [(F32, F32), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("rows,D", [(3, 264), (300, 4096), (5, 8192)])
+def test_residual_norm_backward_without_w_pre_does_not_depend_on_the_stream(rows, D, dtype, res):
+    """Without a norm before the next block r' = a r + s u enters no gradient: infinities and NaN in r change no bit."""
+    for post, gate, scale in ((1, 1, 1), (0, 0, 0), (1, 0, 1)):
+        k = norm_case(rows, D, dtype, res, post, gate, scale, pre=False, seed=D + 2)
+        dr = randn(rows, D, seed=33)
+        run = lambda r: kda.kda_residual_norm_backward(k["y"], r, None, None, dr, w_post=k["w_post"], gate=k["gate"],
+                                                       scale=k["scale"], res_scale=0.75, eps=1e-5)
+        odd = k["r"].clone()
+        odd[0, 5], odd[1, D - 1], odd[rows - 1, 0] = float("inf"), float("-inf"), float("nan")
+        h = {n: host(v) for n, v in k.items()}
+        ref, mag = L.norm_backward(dx=None, dr=host(dr), **h, res_scale=0.75, eps=1e-5), norm_grad_mags(h, None, host(dr))
+        for n, want, got in zip(("dy", "dr", "dgate", "dw_post", "dscale", "dw_pre"), run(k["r"]), run(odd)):
+            assert (want is None) == (got is None) and (got is None or torch.equal(want, got)), n
+            if got is not None:
+                within(got, ref[n], mag[n], 64 + (rows / 8 if n in ("dw_post", "dscale") else 0), n)
+
+
 def test_layer_together():
     """A block as it is used: norm before, convolution, scan, norm after with gate and residual, forwards and
     backwards, every call's outputs the next one's inputs; on a side stream and in a graph the same bits."""
