@@ -299,6 +299,62 @@ def test_ssm_prefill_segments(lengths, ch, n, groups, dtype):
     assert torch.equal(y, again[0]) and torch.equal(S_T, again[1])
 
 
+def ssm_slow_case(lengths, ch, n, groups=1, dtype=F32, seed=0):
+    """Steps so small that a state lasts for segments of 256 tokens (rate times steps of a segment: about 0.1 to 4), larger
+    in some segments than in their neighbours, and initial states that stand out."""
+    k = ssm_case(lengths, ch, n, groups, dtype, seed=seed)
+    t = torch.arange(sum(lengths), device=DEV, dtype=F32).unsqueeze(1)
+    k["dt"] = (randn(sum(lengths), ch, seed=seed + 2, std=0.5, mean=-6.0) + 0.7 * torch.sin(t * (2 * np.pi / 600))).to(dtype)
+    k["S0"] = 8 * k["S0"]
+    return k
+
+
+def ssm_with_join(h, seg, decays):
+    """The scan by segments of `seg` tokens whose join takes decays(steps of the segment, of the one before, A): y, S_T and
+    the segments' first states with their first tokens."""
+    delta = L.softplus(h["dt"] + h["dt_bias"])
+    cuts, seqs = [], []
+    for s, (b, e) in enumerate(zip(h["cu"][:-1], h["cu"][1:])):
+        mine = list(range(b, e, seg)) or [b]
+        cuts += mine
+        seqs += [s] * len(mine)
+    cuts.append(h["cu"][-1])
+    first = [i == 0 or seqs[i - 1] != s for i, s in enumerate(seqs)]
+    start = np.stack([h["S0"][s] if f else np.zeros_like(h["A"]) for s, f in zip(seqs, first)])
+    ends = L.ssm(**{**h, "S0": start, "cu": np.array(cuts)})[1]
+    for i in range(1, len(seqs)):
+        if not first[i]:
+            start[i] = ends[i - 1]
+            if not first[i - 1]:
+                steps = [delta[cuts[j]:cuts[j + 1]].sum(0)[:, None] for j in (i - 1, i - 2)]
+                start[i] += decays(*steps, h["A"]) * start[i - 1]
+    y, S_T = L.ssm(**{**h, "S0": start, "cu": np.array(cuts)})
+    return y, S_T[[i for i in range(len(seqs)) if i + 1 == len(seqs) or first[i + 1]]], start, cuts
+
+
+@pytest.mark.parametrize("lengths,ch,n,groups,dtype", [
+    ([2100], 40, 16, 1, BF16), ([1300, 0, 1030, 3], 24, 8, 1, F32), ([1100], 48, 32, 2, F32), ([1030, 1026], 16, 64, 1, BF16),
+    ([1280], 8, 128, 1, F32)])
+def test_ssm_prefill_segments_carry_their_states(lengths, ch, n, groups, dtype):
+    """States that last for several segments: outputs, final states, tile states, all of which would be far off if a segment's
+    state were not carried on, or carried by another segment's decay."""
+    assert kda.load_library().kda_ssm_prefill_launches(len(lengths), sum(lengths), ch, n, groups) == 3
+    k = ssm_slow_case(lengths, ch, n, groups, dtype, seed=n + 1)
+    y, S_T, tiles = ssm_run(k, save_states=True)
+    ssm_check(k, y, S_T, lengths)
+    tile_states_check(k, tiles, lengths)
+    h = ssm_host(k)
+    (y_ref, S_ref), (y_mag, S_mag), half = L.ssm(**h), ssm_magnitude(h), torch.finfo(dtype).eps / 2
+    long, chain = [m > 512 for m in lengths], (max(lengths) + 64) * 2.0 ** -21
+    bounds = half * np.abs(y_ref) + chain * y_mag, chain * S_mag
+    right = ssm_with_join(h, 256, lambda own, before, A: np.exp(own * A))
+    assert np.allclose(right[0], y_ref, rtol=1e-9, atol=1e-9) and np.allclose(right[1], S_ref, rtol=1e-9, atol=1e-9)
+    for wrong in (lambda own, before, A: 0.0, lambda own, before, A: np.exp(before * A)):
+        y_bad, S_bad = ssm_with_join(h, 256, wrong)[:2]
+        assert (np.abs(y_bad - y_ref) / bounds[0]).max() > 50
+        assert all(o.max() > 20 for o in (np.abs(S_bad - S_ref) / bounds[1])[long])
+
+
 # ------------------------------------------------ selective scan, gradients ----
 
 def ssm_grad_run(k, dy, dS_T, **kw):
@@ -398,6 +454,20 @@ def test_ssm_backward_long_sequences():
     k, dy, dS = ssm_grad_case(lengths, 16, 16, dtype=F32, seed=40)
     assert kda.load_library().kda_ssm_prefill_launches(3, 2000, 16, 16, 1) > 1
     ssm_grad_check(k, dy, dS, ssm_grad_run(k, dy, dS), lengths)
+
+
+def test_ssm_backward_segments_carry_their_states():
+    """Gradients over the tile states of such a forward, whose reverse chains last as long."""
+    lengths = [1300, 0, 1030, 3]
+    k = ssm_slow_case(lengths, 24, 8, seed=45)
+    assert kda.load_library().kda_ssm_prefill_launches(4, 2333, 24, 8, 1) == 3
+    dy, dS = randn(2333, 24, seed=46), 32 * randn(4, 24, 8, seed=47)
+    ssm_grad_check(k, dy, dS, ssm_grad_run(k, dy, dS), lengths)
+    # dS_T reaches the first tokens: without it dS0 would be far off
+    h = ssm_host(k)
+    ref, cut = (L.ssm_backward(dy=host(dy), dS_T=d, **h)["dS0"] for d in (host(dS), None))
+    mag = ssm_grad_magnitude(h, host(dy), host(dS))["dS0"]
+    assert all((np.abs(ref - cut) / (2 * 1300 + 128) / 2.0 ** -21 / mag)[s].max() > 20 for s in (0, 2))
 
 
 def test_ssm_backward_same_bits_and_rows_behind():
