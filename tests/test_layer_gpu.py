@@ -516,6 +516,47 @@ def test_ssm_backward_differences():
         assert abs((up - down) / (2 * h) - want) <= 3e-2 * scale, n
 
 
+@pytest.mark.parametrize("lengths,ch,n,groups,soft", [([90, 40], 16, 16, 1, True), ([65, 1, 0, 30], 16, 8, 2, False)])
+def test_ssm_backward_differences_along_the_gradient(lengths, ch, n, groups, soft):
+    """Each gradient g against the difference of two forward runs along g / |g|, where the slope is |g| itself: another sign,
+    half or twice the size, or a part that points elsewhere shows.
+
+    The difference is off by its truncation (twice the change from half the step, with the formulas in 64 bits: its error
+    falls with the step's square, so that change is three quarters of it) and by the rounding of both runs' outputs (their
+    bounds, added up, over the step). The slope of the kernel's g is off by the bound of g, added up along the direction."""
+    k, dy, dS = ssm_grad_case(lengths, ch, n, groups, seed=42, soft=soft, bias=soft)
+    g, h = ssm_grad_run(k, dy, dS), ssm_host(k)
+    grad_mag, chain, step = ssm_grad_magnitude(h, host(dy), host(dS)), max(lengths) + 64, 0.25
+    hy, hS = host(dy), host(dS)
+
+    def loss(c):
+        y, S = ssm_run(c)
+        return (host(y) * hy).sum() + (host(S) * hS).sum()
+
+    def exact(c):
+        y, S = L.ssm(**ssm_host(c))
+        return (y * hy).sum() + (S * hS).sum()
+
+    y_mag, S_mag = ssm_magnitude(h)
+    for name, of in (("x", "dx"), ("dt", "ddt"), ("B", "dB"), ("C", "dC"), ("z", "dz"), ("A", "dA"), ("D", "dD"),
+                     ("dt_bias", "ddt_bias"), ("S0", "dS0")):
+        if k[name] is None:
+            continue
+        grad = getattr(g, of)
+        size = float(grad.double().norm())
+        move = lambda s: (dict(k, **{name: k[name] + (f * s / size * grad)}) for f in (1, -1))
+        up, down = move(step)
+        along = (host(up[name]) - host(down[name])) / (2 * step)  # as the inputs' rounding leaves it
+        want, got = (host(grad) * along).sum(), (loss(up) - loss(down)) / (2 * step)
+        a, b = [(exact(u) - exact(d)) / (2 * s) for s in (step, step / 2) for u, d in [move(s)]]
+        y_up, S_up = ssm_magnitude(ssm_host(up))
+        outputs = [(np.maximum(u, v) * np.abs(w)).sum() for u, v, w in ((y_up, y_mag, hy), (S_up, S_mag, hS))]
+        tol = 2 * abs(a - b) + 2 * chain * 2.0 ** -21 * sum(outputs) / step \
+            + 2 * chain * 2.0 ** -21 * (grad_mag[of] * np.abs(along)).sum()
+        assert tol < size / 4, "%s: the test cannot tell: %.3g of %.3g" % (name, tol, size)
+        assert abs(got - want) <= tol, "%s: %.6g, by differences %.6g, tolerance %.3g" % (name, want, got, tol)
+
+
 def test_ssm_backward_graph():
     """Captured together with its forward and replayed on other inputs."""
     k, dy, dS = ssm_grad_case([200, 33], 64, 16, dtype=BF16, seed=43)
