@@ -575,6 +575,56 @@ def test_ssm_backward_graph():
         assert torch.equal(u, v)
 
 
+def ssm_in_fp32(h, dy, dS_T):
+    """S_T, dS0 and dA of one sequence (one group) as the formulas give them token by token with every operation rounded to
+    fp32, but for the exponentials of the states' chain: those err as the hardware's do.
+
+    The hardware's 2^x was measured against fp64 at a million points of each [-2^e, -2^(e-1)], e = -15 .. 1: off by at most
+    2^-22.7 of itself, and too small on average: by at most 8e-9 above -2^-8, 2.7e-8 down to -1/4, 5.1e-8 below. So here,
+    with a uniform part of up to 2^-22.7."""
+    rng, f = np.random.default_rng(0), np.float32
+    x, dt, B, C, A, z, bias = (h[n].astype(f) for n in ("x", "dt", "B", "C", "A", "z", "dt_bias"))
+    delta, e = L.softplus(dt + bias), dy.astype(f) * z * L.sigmoid(z)
+    S, G, dA, block, before, a = h["S0"][0].astype(f), dS_T[0].astype(f), np.zeros_like(A), np.zeros_like(A), [], []
+    for t in range(len(x)):
+        before.append(S)
+        a.append(np.exp(delta[t][:, None] * A))
+        v = np.float64(delta[t][:, None] * A)
+        low = np.where(v > -2.0 ** -8 * np.log(2), 8e-9, np.where(v > -0.25 * np.log(2), 2.7e-8, 5.1e-8))
+        S = ((1 - low + 2.0 ** -22.7 * rng.uniform(-1, 1, A.shape)) * np.exp(v) * S + (delta[t] * x[t])[:, None] * B[t]).astype(f)
+    for t in range(len(x) - 1, -1, -1):
+        G = a[t] * (G + C[t] * e[t][:, None])
+        block = block + G * before[t] * delta[t][:, None]
+        if t % 128 == 0:
+            dA, block = dA + block, np.zeros_like(block)
+    assert all(v.dtype == f for v in (S, G, dA))
+    return S, G, dA
+
+
+@pytest.mark.parametrize("T,n,mean", [(500, 16, -6.0), (1422, 8, -4.0), (1422, 16, -6.0)])
+def test_ssm_long_chains_keep_their_bits(T, n, mean):
+    """Slow decays over one long sequence in fp32, by norm: S_T, dS0 and dA are off by at most twice what rounding each
+    operation to fp32 leaves, with the hardware's exponentials in the states' chain and exact ones in the gradients' own.
+
+    S_T comes through the states' chain alone and dS0 through the gradients' alone (the hardware's exponentials there would
+    leave 3 to 5 times as much). dA = sum_t delta_t G_t a_t h_(t-1) takes one factor from each: a relative error of h_(t-1)
+    is one of the term, and one that leans to one side, a step's worth for every step that a part of h_(t-1) has come
+    through, does not average out over the tokens. So the states' exponentials count in dA as they do in S_T."""
+    ch = 64
+    k = ssm_case([T], ch, n, seed=76)
+    k["dt"] = randn(T, ch, seed=79, std=0.5, mean=mean)
+    dy, dS = randn(T, ch, seed=80), randn(1, ch, n, seed=81)
+    g, S_T, h = ssm_grad_run(k, dy, dS), ssm_run(k)[1], ssm_host(k)
+    ref, S_ref = L.ssm_backward(dy=host(dy), dS_T=host(dS), **h), L.ssm(**h)[1]
+    error = lambda got, want: np.linalg.norm(got - want) / np.linalg.norm(want)
+    model = ssm_in_fp32(h, host(dy), host(dS))
+    for name, got, want, m in (("S_T", S_T[0], S_ref[0], model[0]), ("dS0", g.dS0[0], ref["dS0"][0], model[1]),
+                               ("dA", g.dA, ref["dA"], model[2])):
+        have, allow = error(host(got), want), 2 * error(m, want)
+        print("%s: %.2e of its norm, allowed %.2e" % (name, have, allow))
+        assert have <= allow, "%s: %.3g of its norm, allowed %.3g" % (name, have, allow)
+
+
 # ----------------------------------------------------------- short convolution ----
 # A sum of W products and a bias: (W + 1) 2^-24 of its terms' magnitude, through a Swish whose slope is at
 # most 1.1, its exponential and reciprocal good to 2^-22 each: chain 4 W + 16 steps of 2^-21 covers it. dw
