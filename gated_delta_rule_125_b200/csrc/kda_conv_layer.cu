@@ -10,10 +10,11 @@
 // All of it is bound by memory: x (and dy) read once, y (dx) written once. A thread owns 4 consecutive
 // channels of a run of consecutive tokens and keeps the window in registers (8 channels halve the loads and
 // double the registers: 117 us against 85 us for an earlier backward of 8192 tokens x 4096 channels, W = 4).
-// It loads some rows ahead, so that enough bytes are in flight: the forward (32 us for that size, 64 % of the
-// copy rate, its exponentials and reciprocals at 54 % of theirs) to registers, the backward, which has none left,
-// to shared memory (60 us, 68 %; to registers and none further ahead 85 us). The rows around its run that its
-// window needs are its neighbours' too and come from the L2 cache.
+// It loads some rows ahead, so that bytes are in flight: the forward (32 us for that size, 64 % of the copy rate;
+// it waits for those loads, its schedulers issue in 56 % of the clocks, its exponentials and reciprocals run at 49 %
+// of their rate) to registers, the backward, which has none left, to shared memory (60 us with an fp32 dy, 85 % of
+// the copy rate; to registers and none further ahead 85 us). The rows around its run that its window needs are its
+// neighbours' too and come from the L2 cache.
 #include <type_traits>
 
 #include "kda_layer.cuh"

@@ -365,7 +365,8 @@ int64_t ctas_of(int64_t rows, int threads, int most, int per_sm) {
 }
 
 // Forward: 256 threads of up to two vectors, three CTAs to an SM, up to 4096 channels (61 us for 8192 rows
-// of 4096 bf16 channels with a gate, 83 % of the copy rate; 512 threads of one vector, two CTAs: 70 us).
+// of 4096 bf16 channels with a gate, 83 % of the copy rate; 512 threads of one vector, two CTAs: 70 us). Three CTAs
+// cap the registers at 80: from 2056 channels on 40 bytes a thread spill with an fp32 stream, 232 in all fp32.
 template <typename T, typename R> cudaError_t launch(const NormArgs &a, cudaStream_t st) {
     if (a.rows == 0) return cudaSuccess;
     if (a.D <= 4096) {

@@ -380,9 +380,9 @@ ssm_join_kernel(const SsmArgs a, const int L, float *__restrict__ seg_state, con
 
 // How the lanes and the time axis are dealt out.
 constexpr int kMinSegment = 256;
-// Lanes of a channel (on one GPU). 16 states: four lanes 342 us for 8192 tokens of 4096 channels, eight 355 us
-// (fewer shuffles against more warps). 64 states: eight lanes 158 us for 6151 tokens of 1024 channels in 16
-// sequences, sixteen 225 us.
+// Lanes of a channel (in turn on one GPU). 16 states: four lanes 324 us for 8192 tokens of 4096 channels, eight
+// 356 us (fewer shuffles against more warps). 64 states: eight lanes 156 us for 6151 tokens of 1024 channels in 16
+// sequences, sixteen 179 us.
 constexpr int lanes_of(int states) { return states <= 16 ? 4 : 8; }
 struct Cut {
     int L;  // tokens of a segment
@@ -391,7 +391,9 @@ struct Cut {
     bool split;
 };
 // The time axis is cut where the sequences' channels give a CTA to fewer than half of the SMs: a cut takes
-// the exponentials twice (8192 tokens of 4096 channels, 128 CTAs: 342 us uncut, 420 us in four segments).
+// the exponentials twice (8192 tokens of 4096 channels, 128 CTAs: 324 us uncut, 424 us in four segments).
+// The rule counts sequences, not their tokens: a batch of one long prompt and many short ones of few channels
+// stays uncut.
 Cut cut_of(int64_t total, int N, int channels, int states, int groups) {
     const int CB = kScanThreads / lanes_of(states);
     Cut c;
@@ -466,7 +468,8 @@ cudaError_t ssm_prefill(const SsmArgs &a, void *ws, bool bf16, cudaStream_t st) 
 // sequences; a lane holds U 4-state vectors of them, n / 4 lanes to a channel, so every access is
 // a run of 16-byte vectors. The per-channel work (softplus, gate) is done by one lane per channel
 // and handed over by shuffles; C h is summed over a channel's lanes by shuffles. Measured, 256 sequences
-// x 4096 channels x 16 states in bf16 (143 MB): 28 to 31 us, 70 to 77 % of the copy rate.
+// x 4096 channels x 16 states in bf16 (143 MB): 28 to 31 us, 70 to 77 % of the copy rate. Six CTAs to an SM cap
+// the registers at 80: 20 to 36 bytes a thread spill at 16 to 128 states.
 namespace {
 
 constexpr int kStepThreads = 128, kStepPerSm = 6;

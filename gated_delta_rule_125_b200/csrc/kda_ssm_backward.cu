@@ -24,11 +24,13 @@
 // them in a fixed order: no atomics, the same bits every time.
 //
 // Measured, 4096 tokens (the longest sequence 2853) x 4096 channels x 16 states, bf16 with a gate: 694 us
-// with 24 more for the sums over the channels. Two warps per SM quarter (224 registers) issue in 52 % of the
+// with 24 more for the sums over the channels. Two warps per SM quarter (221 registers) issue in 52 % of the
 // clocks; the shared memory's pipe is 56 % busy, half of that with shuffles. What it replaced: every load
 // waited for where it is used 735 us, with B and C expanded to fp32 in shared memory; three CTAs to an SM
 // (registers capped without spills) 790 us, as the longest sequence's chain then gets a third of an SM (8
-// sequences of 512 tokens, which balance: 734 us with two CTAs, 703 us with three).
+// sequences of 512 tokens, which balance: 734 us with two CTAs, 703 us with three). At 32 and at 128 states the
+// states before the groups take 64 and 80 KB of shared memory (127 to 131 KB in all), so that only one CTA fits an
+// SM there; the sizes above were measured at 16 states.
 #include "kda_layer.cuh"
 
 namespace kda {

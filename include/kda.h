@@ -377,9 +377,12 @@ kda_status kda_backward(const void *q, const void *k, const void *v, const float
  *
  * where g is the channel's group: `groups` runs of channels / groups channels share B and C. x is
  * usually the output of the short convolution (kda_short_conv_swish). Arithmetic is fp32 for both
- * dtypes; outputs are rounded once. Exponentials of delta A have a relative error of about 2^-22.
+ * dtypes; outputs are rounded once. Exponentials of delta A are the hardware's: their relative error is
+ * at most about 2^-22 + |delta A| 2^-23 (delta A log2 e is rounded twice on the way), and near 1 they
+ * are 5e-9 to 3e-8 too small on average, so that a state which lasts for M tokens is off by about M times
+ * that. The gradients' own chain takes a more exact exponential.
  *
- *   channels   a multiple of 8 * groups
+ *   channels   a multiple of 8 * groups, at most 65536 (KDA_ERR_UNSUPPORTED otherwise)
  *   states     8, 16, 32, 64 or 128 (KDA_ERR_UNSUPPORTED otherwise)
  *   A          [channels][states] fp32, 16-byte aligned (decay rates: finite, normally < 0)
  *   D          [channels] fp32 or NULL (0);  dt_bias [channels] fp32 or NULL (0); 4-byte aligned
@@ -472,8 +475,9 @@ kda_status kda_ssm_backward(const void *x, const void *dt, const void *B, const 
 
 /*
  * kda_short_conv_swish with a bias: y_t[c] = v sigmoid(v), v = bias[c] + z_t[c] (z as above); bias [C]
- * fp32, 4-byte aligned (NULL: none, then the same values as kda_short_conv_swish to rounding). Rows
- * from cu_seqlens[N] on are neither read nor written. Launches as kda_short_conv_launches().
+ * fp32, 4-byte aligned (NULL: none, then the same values as kda_short_conv_swish to rounding), C at most
+ * 2^20 (so for the step and the backward). Rows from cu_seqlens[N] on are neither read nor written.
+ * Launches as kda_short_conv_launches().
  */
 kda_status kda_short_conv_swish_ex(const void *x, void *y, const kda_short_conv *conv, const float *bias,
                                    const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
@@ -498,7 +502,8 @@ kda_status kda_short_conv_step(const void *x, void *y, const kda_short_conv *con
  * Rows from cu_seqlens[N] on are neither read nor written. dweight and dbias are summed in a fixed
  * order (no atomics). dx must not overlap x or dy (KDA_ERR_INVALID_ARG), no output may overlap an input.
  * workspace: kda_short_conv_backward_workspace_size() bytes (a partial dweight and dbias per 32 tokens, or
- * per longer runs where those fill the GPU). Two launches, three with dstate and cu_seqlens.
+ * per longer runs where those fill the GPU). Two launches (one without tokens), one more with dstate where
+ * a sequence may be empty.
  */
 size_t kda_short_conv_backward_workspace_size(int64_t total_tokens, int32_t channels, int32_t width);
 kda_status kda_short_conv_backward(const void *x, const kda_short_conv *conv, const float *bias,
@@ -519,7 +524,7 @@ kda_status kda_short_conv_backward(const void *x, const kda_short_conv *conv, co
  *   w_post, scale, w_pre  [D] fp32       D a multiple of 8, at most KDA_MAX_NORM_CHANNELS
  *
  * All 16-byte aligned. x is computed from r_out before its rounding. r_out may be r; no other output may
- * overlap an input. Arithmetic is fp32. One launch.
+ * overlap an input. Arithmetic is fp32. One launch (none without rows).
  */
 #define KDA_MAX_NORM_CHANNELS 8192
 typedef struct kda_residual_norm_args {
@@ -545,7 +550,7 @@ kda_status kda_residual_norm(const kda_residual_norm_args *args, void *x, void *
  * [rows][D] (NULL iff gate is); dw_post, dscale, dw_pre [D] or NULL (not written; NULL where the weight
  * is). dr may be dr_out; no other output may overlap an input. All 16-byte aligned. Column sums are
  * added in a fixed order (no atomics). workspace: kda_residual_norm_backward_workspace_size() bytes.
- * Two launches.
+ * Two launches (one where no weight gradient is asked for). Without w_pre no gradient depends on r.
  */
 size_t kda_residual_norm_backward_workspace_size(int64_t rows, int32_t D);
 kda_status kda_residual_norm_backward(const kda_residual_norm_args *args, const void *dx, const float *dr_out,
